@@ -398,6 +398,136 @@ zero_status zero_offload_step(const zero_grad_src* src, uint64_t n, float grad_s
                               void* d_out_param, int32_t out_dtype,
                               const zero_offload_buffers* buf, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The layer between the gather and the gradient rows. A ZeRO-3 rank gathers a layer, runs it,
+ * releases it, and gathers it again for its backward, whose gradients are what the reduction sums
+ * (P1 section 三; P2 ZeRO Stage 3). The pages name these passes and print none of their
+ * arithmetic; the operators below are stated in full here. They read parameters in place in a gathered buffer and write parameter
+ * gradients in place into a replica row, both at any element offset.
+ * Matrices are row-major: element (i, j) of a matrix with leading dimension ld lies at i*ld + j,
+ * ld >= its columns (not looked at for a single row). Parameters and their gradients are
+ * contiguous (ld = in_features), as they lie in the flat space. 16-bit results are rounded once,
+ * to nearest even, from an fp32 value. Every array may start at any multiple of its element size;
+ * arrays and rows on 16 bytes are the fast ones. */
+
+typedef enum {
+  ZERO_ACT_NONE = 0,
+  ZERO_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */
+  ZERO_ACT_GELU = 2,      /* z * (1 + erf(z/sqrt(2))) / 2 */
+  ZERO_ACT_GELU_TANH = 3, /* z * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) / 2 */
+  ZERO_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} zero_act;
+
+typedef struct {
+  uint64_t rows;         /* tokens */
+  uint64_t in_features;
+  uint64_t out_features;
+  int32_t dtype;         /* ZERO_BF16 or ZERO_F16: activations, parameters and their 16-bit gradients */
+  int32_t act;           /* zero_act */
+} zero_linear_shape;
+
+/* Bytes of device workspace that zero_linear_forward (backward == 0) or zero_linear_backward
+ * (backward != 0) of this many rows and features needs, for any dtype, activation, outputs and
+ * alignment; 0 for none. The workspace must start on 16 bytes, holds nothing between calls and
+ * needs no clearing; calls that may overlap in time (other streams, graphs replayed at once) need
+ * one each. Host only; never fails (sizes the calls refuse give 0). */
+uint64_t zero_linear_workspace_bytes(uint64_t rows, uint64_t in_features, uint64_t out_features,
+                                     int32_t backward);
+
+/* A linear layer with its epilogue:
+ *   z = x W^T + bias;  pre = round16(z);  y = round16(act(z) + residual)
+ * x [rows, in], weight W [out, in] contiguous, bias [out] (nullable), residual [rows, out]
+ * (nullable), pre [rows, out] (nullable; what zero_linear_backward needs of a layer with an
+ * activation), y [rows, out]; all of s->dtype. Products are exact, sums fp32 in a fixed order, and
+ * y comes from the unrounded z. rows == 0 or out_features == 0 enqueues nothing; in_features == 0
+ * is the empty sum.
+ * Aliasing: y may be the residual itself (same pointer and ldy == ldr); otherwise y, pre and the
+ * workspace must not overlap any array of the call. Column slices of one buffer do not overlap.
+ * Errors: NULLs, a leading dimension below the columns, aliasing, an unknown act, an array off its
+ * element size, a workspace that is missing, too small or off 16 bytes -> ZERO_E_INVAL; dtype
+ * ZERO_F32 -> ZERO_E_UNSUPPORTED; a size above 2^31 - 1 or a byte count >= 2^63 ->
+ * ZERO_E_OVERFLOW. */
+zero_status zero_linear_forward(const zero_linear_shape* s, const void* x, uint64_t ldx,
+                                const void* weight, const void* bias, const void* residual,
+                                uint64_t ldr, void* pre, uint64_t ldp, void* y, uint64_t ldy,
+                                void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* The gradients of zero_linear_forward from dy = dL/dy [rows, out]:
+ *   dz = round16(dy * act'(pre))   (dz = dy itself, unwritten, for ZERO_ACT_NONE)
+ *   dx = round16(dz W);  dweight = dz^T x;  dbias = sum over rows of dz
+ * with the sums fp32 in a fixed order; the residual's gradient is dy. With an activation, pre and
+ * dz [rows, out] are required (without one both are ignored). dx [rows, in], dweight [out, in]
+ * contiguous and dbias [out]: any subset, at least one of the three or, with an activation, none.
+ * x is needed for dweight, weight for dx. dweight and dbias are of grad_dtype (s->dtype or
+ * ZERO_F32), e.g. inside a replica row that zero_reduce_shard will sum; with accumulate != 0 the
+ * sum is added to what they hold (in fp32, then rounded once). rows == 0 zeroes dweight and dbias
+ * (leaves them with accumulate); out_features == 0 zeroes dx.
+ * Aliasing: dz may be dy or pre itself (same pointer and leading dimension); otherwise dz, dx,
+ * dweight, dbias and the workspace must not overlap any array of the call.
+ * Errors: as zero_linear_forward; grad_dtype neither dtype nor ZERO_F32 -> ZERO_E_UNSUPPORTED. */
+zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uint64_t lddy,
+                                 const void* x, uint64_t ldx, const void* weight, const void* pre,
+                                 uint64_t ldp, void* dz, uint64_t lddz, void* dx, uint64_t lddx,
+                                 void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
+                                 void* workspace, uint64_t workspace_bytes, void* stream);
+
+#define ZERO_DISTILL_MAX_TOPK 1024     /* teacher entries of one row */
+#define ZERO_DISTILL_MAX_VOCAB 393216  /* logits of one row */
+
+/* The inputs of the distillation loss: a student's logits and, per row, a teacher's top entries. */
+typedef struct {
+  uint64_t rows, vocab, topk;
+  int32_t logit_dtype;        /* zero_dtype of logits and of their gradient */
+  int32_t teacher_dtype;      /* zero_dtype of top_logits */
+  int32_t index_bytes;        /* 4 (int32) or 8 (int64) */
+  float temperature;          /* T, 2^-20 to 2^20 */
+  const void* logits;         /* [rows, vocab], leading dimension ld_logits */
+  uint64_t ld_logits;
+  const void* top_index;      /* [rows, topk], leading dimension ld_top */
+  const void* top_logits;     /* [rows, topk], leading dimension ld_top */
+  uint64_t ld_top;
+  const float* tail;          /* [rows] or NULL: log of the sum of exp(t/T) over the teacher's
+                                 entries that are not listed (-inf: none) */
+  const float* weight;        /* [rows] or NULL (1): a row of weight 0 is not read */
+} zero_distill_in;
+
+/* Distillation from a teacher's top logits. With z a row's logits, (i_k, t_k) its teacher entries:
+ *   q = softmax(z / T);  p = softmax over k of t_k / T, with the tail as one more entry if given
+ *   loss = weight * ( sum_k p_k (log p_k - log q[i_k]) + [tail] p_tail (log p_tail - log q_rest) )
+ * where q_rest is the student's mass outside the listed entries. Terms with p_k = 0 are 0. Without
+ * a tail the listed entries are the whole teacher; one entry per row, at T = 1, is the cross entropy
+ * of a hard label.
+ * An entry whose index lies outside [0, vocab) is no entry (use -1 for short rows), and one of
+ * logit -inf has p = 0. An index listed twice counts with both its p. A row with no teacher mass
+ * at all (no entry, all -inf) and a row of weight 0 have loss 0 and gradient 0. Logits of -inf
+ * are entries of no mass; a row with a NaN, a +inf or nothing but -inf has no softmax: its
+ * loss and gradient are NaN. A loss may be +inf (mass of p where q has none).
+ * loss: device float[rows]. stats: device float[2*rows], what the backward needs of the row
+ * (opaque). Sums are fp32 in a fixed order. rows == 0 enqueues nothing.
+ * Errors: NULLs, topk or vocab 0, index_bytes not 4 or 8, T out of its range, a leading dimension
+ * below the columns, an array off its element size, loss or stats overlapping any array of the
+ * call -> ZERO_E_INVAL; unknown dtypes, topk or vocab above the limits ->
+ * ZERO_E_UNSUPPORTED; rows above 2^31 - 1 or a byte count >= 2^63 -> ZERO_E_OVERFLOW. */
+zero_status zero_distill_forward(const zero_distill_in* in, float* loss, float* stats, void* stream);
+
+/* The loss's gradient in the logits, from the stats of zero_distill_forward over the same inputs:
+ *   dlogits[r, v] = scale * upstream[r] * dloss[r]/dz[r, v]
+ *   dloss/dz_v = weight/T * (q_v - p_v), p_v the p of all entries listing v; with a tail, for v in
+ *   no entry, weight/T * q_v * (1 - p_tail / q_rest)
+ * scale is where a loss scale, a mean over tokens and T^2 go; upstream (device float[rows], nullable)
+ * is 1 without. dlogits [rows, vocab] of logit_dtype, leading dimension ld_dlogits; it may be the
+ * logits themselves (same pointer and leading dimension), and otherwise overlaps nothing of the
+ * call. Errors: as zero_distill_forward; scale not finite -> ZERO_E_INVAL. */
+zero_status zero_distill_backward(const zero_distill_in* in, const float* stats,
+                                  const float* upstream, float scale, void* dlogits,
+                                  uint64_t ld_dlogits, void* stream);
+
+/* zero_distill_forward and zero_distill_backward in one pass over the logits, for a step that
+ * knows its scale beforehand: loss[r] as the one writes it, dlogits as the other. Errors and
+ * aliasing: as theirs. */
+zero_status zero_distill_step(const zero_distill_in* in, const float* upstream, float scale,
+                              float* loss, void* dlogits, uint64_t ld_dlogits, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* zero_status_str(zero_status s);
 

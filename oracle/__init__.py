@@ -25,6 +25,8 @@ Modules:
   gather     ZeRO-3 gather of one layer's parameters from the rank shards         [P1 三; P3 core operations]
   memory     per-stage model-state bytes per rank (DP, ZeRO-1/2/3), the bytes a
              rank sends per step under each stage, and the stage-choice rule  [P1 一/二/三/四; P3 stages]
+  layer      a linear layer and the top-logit distillation loss with their gradients, in fp64
+             (the passes a gathered layer runs: [P1 三; P2 Stage 3]; arithmetic not on the pages)
 
 Parity status of each function is stated in its docstring. The clip coefficient has no page; its
 reading is pinned against torch.nn.utils.clip_grad_norm_, a library implementation of the rule.
@@ -45,6 +47,7 @@ from .adam import (
     unsharded_step,
 )
 from .gather import gather_range
+from . import layer
 from .memory import (MemoryEstimation, estimate_memory_per_gpu, stage_bytes_exact, stage_comm_bytes, STAGES,
                      choose_stage)
 
@@ -53,7 +56,7 @@ __all__ = [
     "cast_bf16_rne", "cast_fp16_rne", "widen_bf16", "widen_fp16",
     "AdamHParams", "AdamScalars", "adam_scalars", "adam_update", "replica_sum",
     "nonfinite_flag", "shard_sqnorm", "clip_coefficient", "sharded_step", "unsharded_step",
-    "gather_range",
+    "gather_range", "layer",
     "MemoryEstimation", "estimate_memory_per_gpu", "stage_bytes_exact", "stage_comm_bytes", "STAGES",
     "choose_stage",
 ]

@@ -30,6 +30,10 @@ __all__ = [
     "zero_adam_shard_step_dev_t",
     "AdamStep", "ReduceCall",
     "zero_gather_params", "zero_host_adam_step", "zero_offload_step",
+    "ZeroLinearShape", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_GELU_TANH",
+    "ZERO_ACT_SILU", "zero_linear_workspace_bytes", "zero_linear_forward", "zero_linear_backward",
+    "ZeroDistillIn", "ZERO_DISTILL_MAX_TOPK", "ZERO_DISTILL_MAX_VOCAB", "zero_distill_forward",
+    "zero_distill_backward", "zero_distill_step",
     "zero_status_str", "zero_last_error",
 ]
 
@@ -39,6 +43,9 @@ ZERO_OK, ZERO_E_INVAL, ZERO_E_OVERFLOW, ZERO_E_UNSUPPORTED, ZERO_E_HIP = range(5
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_ADAMW, ZERO_ADAM_L2 = 0, 1
 ZERO_DEV_T_OUT_OF_TABLE = 1
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU = range(5)
+ZERO_DISTILL_MAX_TOPK = 1024
+ZERO_DISTILL_MAX_VOCAB = 393216
 ZERO_STATIC_SQ_PARTIALS = 4 << 20
 ZERO_STATIC_MAX_ELEMS = (ZERO_STATIC_SQ_PARTIALS - 1024) * 256
 
@@ -93,6 +100,20 @@ class ZeroAdamScalars(ctypes.Structure):
     _fields_ = [(k, ctypes.c_float) for k in ("b1", "b2", "c1", "c2", "ss", "bc", "e", "dec", "w")]
 
 
+class ZeroLinearShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("in_features", ctypes.c_uint64),
+                ("out_features", ctypes.c_uint64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class ZeroDistillIn(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("topk", ctypes.c_uint64),
+                ("logit_dtype", ctypes.c_int32), ("teacher_dtype", ctypes.c_int32),
+                ("index_bytes", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_uint64),
+                ("top_index", ctypes.c_void_p), ("top_logits", ctypes.c_void_p),
+                ("ld_top", ctypes.c_uint64), ("tail", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
+
+
 def adam_hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, wd_mode="adamw",
                  step=1) -> ZeroAdamHParams:
     mode = {"adamw": ZERO_ADAMW, "l2": ZERO_ADAM_L2}.get(wd_mode, wd_mode)
@@ -143,6 +164,13 @@ def lib() -> ctypes.CDLL:
                                     u32],
             "zero_offload_step": [P(_GradSrc), u64, ctypes.c_float, vp, vp, vp, P(ZeroAdamHParams),
                                   vp, i32, P(ZeroOffloadBuffers), vp],
+            "zero_linear_forward": [P(ZeroLinearShape), vp, u64, vp, vp, vp, u64, vp, u64, vp, u64,
+                                    vp, u64, vp],
+            "zero_linear_backward": [P(ZeroLinearShape), vp, u64, vp, u64, vp, vp, u64, vp, u64, vp,
+                                     u64, vp, vp, i32, i32, vp, u64, vp],
+            "zero_distill_forward": [P(ZeroDistillIn), vp, vp, vp],
+            "zero_distill_backward": [P(ZeroDistillIn), vp, vp, ctypes.c_float, vp, u64, vp],
+            "zero_distill_step": [P(ZeroDistillIn), vp, ctypes.c_float, vp, vp, u64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -150,6 +178,8 @@ def lib() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         L.zero_sq_partials_len.argtypes = [u64]
         L.zero_sq_partials_len.restype = u64
+        L.zero_linear_workspace_bytes.argtypes = [u64, u64, u64, i32]
+        L.zero_linear_workspace_bytes.restype = u64
         L.zero_status_str.argtypes = [ctypes.c_int]
         L.zero_status_str.restype = ctypes.c_char_p
         L.zero_last_error.argtypes = []
@@ -503,6 +533,181 @@ def zero_gather_params(shards, begin: int, count: int, out, stream=None):
     _check(lib().zero_gather_params(ctypes.cast(arr, ctypes.POINTER(ctypes.c_void_p)), len(rows), S, eb,
                                     begin, count, _ptr(out, count, "out"), _stream(stream)),
            "zero_gather_params")
+
+
+# ------------------------------------------------------------------------------ layer and loss calls
+
+_ACTS = {"none": ZERO_ACT_NONE, "relu": ZERO_ACT_RELU, "gelu": ZERO_ACT_GELU,
+         "gelu_tanh": ZERO_ACT_GELU_TANH, "silu": ZERO_ACT_SILU}
+
+
+def _here(t, what: str):
+    """The library launches on the current device: a tensor elsewhere is refused."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _mat(t, rows: int, cols: int, what: str, dtype) -> tuple[int | None, int]:
+    """(address, leading dimension) of a row-major (rows, cols) device matrix, or (None, cols)."""
+    if t is None:
+        return None, cols
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, {dtype} expected")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, ({rows}, {cols}) expected")
+    if cols > 1 and t.numel() and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be adjacent")
+    _here(t, what)
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _vec(t, n: int, what: str, dtype) -> int | None:
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, {dtype} expected")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous elements expected")
+    _here(t, what)
+    return t.data_ptr()
+
+
+def _param(t, rows: int, cols: int, what: str, dtype) -> int | None:
+    """A parameter or its gradient: (rows, cols), contiguous, as it lies in the flat space."""
+    ptr, ld = _mat(t, rows, cols, what, dtype)
+    if t is not None and rows > 1 and cols and ld != cols:
+        raise ValueError(f"{what} must be contiguous")
+    return ptr
+
+
+def _workspace(t) -> tuple[int | None, int]:
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+        raise TypeError("workspace must be a contiguous device tensor")
+    _here(t, "workspace")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _linear_shape(x, weight, rows: int, act) -> ZeroLinearShape:
+    kind = _ACTS.get(act, act)
+    if not isinstance(kind, int):
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(_ACTS)}")
+    if weight.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("the linear layer takes bfloat16 or float16")
+    return ZeroLinearShape(rows, weight.shape[1], weight.shape[0], _TORCH_DT[weight.dtype], kind)
+
+
+def zero_linear_workspace_bytes(rows: int, in_features: int, out_features: int,
+                                backward: bool = False) -> int:
+    """Bytes of device workspace the linear layer's forward or backward of this size needs."""
+    return int(lib().zero_linear_workspace_bytes(rows, in_features, out_features, int(backward)))
+
+
+def zero_linear_forward(x, weight, out, bias=None, residual=None, act="none", pre=None,
+                        workspace=None, stream=None):
+    """out = act(x @ weight.T + bias) + residual, and pre = the argument of act (both optional inputs
+    and ``pre`` may be None). ``x`` (rows, in), ``weight`` (out, in) contiguous, e.g. a view of the
+    gathered layer; ``workspace``: a device tensor of zero_linear_workspace_bytes."""
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor) or x.dim() != 2 or weight.dim() != 2:
+        raise TypeError("x and weight must be 2-D device tensors")
+    dt = weight.dtype
+    s = _linear_shape(x, weight, x.shape[0], act)
+    M, K, N = s.rows, s.in_features, s.out_features
+    if out is None:
+        raise TypeError("out must be a device tensor")
+    _check(lib().zero_linear_forward(
+        ctypes.byref(s), *_mat(x, M, K, "x", dt), _param(weight, N, K, "weight", dt),
+        _vec(bias, N, "bias", dt), *_mat(residual, M, N, "residual", dt), *_mat(pre, M, N, "pre", dt),
+        *_mat(out, M, N, "out", dt), *_workspace(workspace), _stream(stream)), "zero_linear_forward")
+
+
+def zero_linear_backward(dy, x, weight, act="none", pre=None, dz=None, dx=None, dweight=None,
+                         dbias=None, accumulate: bool = False, workspace=None, stream=None):
+    """The gradients of zero_linear_forward. With an activation ``dz`` receives dy * act'(pre) (it may
+    be ``dy`` or ``pre`` itself); ``dx`` (rows, in), ``dweight`` (out, in) contiguous and ``dbias``
+    (out), each optional; the last two of weight's dtype or float32, e.g. views of a replica row,
+    and added to with ``accumulate``."""
+    for t in (dy, x, weight):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise TypeError("dy, x and weight must be 2-D device tensors")
+    dt = weight.dtype
+    s = _linear_shape(x, weight, dy.shape[0], act)
+    M, K, N = s.rows, s.in_features, s.out_features
+    grads = [t for t in (dweight, dbias) if t is not None]
+    gdt = grads[0].dtype if grads else dt
+    if gdt not in _TORCH_DT:
+        raise TypeError("dweight and dbias: the weight's dtype or float32")
+    _check(lib().zero_linear_backward(
+        ctypes.byref(s), *_mat(dy, M, N, "dy", dt), *_mat(x, M, K, "x", dt),
+        _param(weight, N, K, "weight", dt), *_mat(pre, M, N, "pre", dt), *_mat(dz, M, N, "dz", dt),
+        *_mat(dx, M, K, "dx", dt), _param(dweight, N, K, "dweight", gdt), _vec(dbias, N, "dbias", gdt),
+        _TORCH_DT[gdt], int(bool(accumulate)), *_workspace(workspace), _stream(stream)),
+        "zero_linear_backward")
+
+
+def _distill_in(logits, top_index, top_logits, temperature, tail, weight) -> ZeroDistillIn:
+    for t, what in ((logits, "logits"), (top_index, "top_index"), (top_logits, "top_logits")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise TypeError(f"{what} must be a 2-D device tensor")
+    if logits.dtype not in _TORCH_DT or top_logits.dtype not in _TORCH_DT:
+        raise TypeError("logits and top_logits must be float32, float16 or bfloat16")
+    if top_index.dtype not in (torch.int32, torch.int64):
+        raise TypeError("top_index must be int32 or int64")
+    R, V = logits.shape
+    K = top_index.shape[1]
+    if tuple(top_index.shape) != (R, K) or tuple(top_logits.shape) != (R, K):
+        raise ValueError("top_index and top_logits must be (rows, topk) alike")
+    lp, ldl = _mat(logits, R, V, "logits", logits.dtype)
+    ip, ldi = _mat(top_index, R, K, "top_index", top_index.dtype)
+    tp, ldt = _mat(top_logits, R, K, "top_logits", top_logits.dtype)
+    if ldi != ldt:
+        raise ValueError("top_index and top_logits must have the same row stride")
+    f32 = torch.float32
+    return ZeroDistillIn(R, V, K, _TORCH_DT[logits.dtype], _TORCH_DT[top_logits.dtype],
+                         top_index.element_size(), float(temperature), lp, ldl, ip, tp, ldt,
+                         _vec(tail, R, "tail", f32), _vec(weight, R, "weight", f32))
+
+
+def zero_distill_forward(logits, top_index, top_logits, temperature: float, loss, stats, tail=None,
+                         weight=None, stream=None):
+    """loss[r] = weight[r] * KL(teacher || student) over the teacher's top entries of row r (an entry
+    of index -1 is none; ``tail``: the log of the teacher's remaining mass, float32). ``loss``:
+    float32 (rows,); ``stats``: float32 (rows, 2), kept for zero_distill_backward."""
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
+    f32 = torch.float32
+    _check(lib().zero_distill_forward(ctypes.byref(a), _vec(loss, a.rows, "loss", f32),
+                                      _vec(stats, 2 * a.rows, "stats", f32), _stream(stream)),
+           "zero_distill_forward")
+
+
+def zero_distill_backward(logits, top_index, top_logits, temperature: float, stats, dlogits, tail=None,
+                          weight=None, upstream=None, scale: float = 1.0, stream=None):
+    """dlogits = scale * upstream[r] * the gradient of loss[r] (``upstream``: float32 (rows,) or None);
+    ``dlogits`` may be ``logits`` itself."""
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
+    f32 = torch.float32
+    _check(lib().zero_distill_backward(
+        ctypes.byref(a), _vec(stats, 2 * a.rows, "stats", f32), _vec(upstream, a.rows, "upstream", f32),
+        float(scale), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype), _stream(stream)),
+        "zero_distill_backward")
+
+
+def zero_distill_step(logits, top_index, top_logits, temperature: float, loss, dlogits, tail=None,
+                      weight=None, upstream=None, scale: float = 1.0, stream=None):
+    """zero_distill_forward and zero_distill_backward in one pass over the logits."""
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
+    f32 = torch.float32
+    _check(lib().zero_distill_step(
+        ctypes.byref(a), _vec(upstream, a.rows, "upstream", f32), float(scale),
+        _vec(loss, a.rows, "loss", f32), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype),
+        _stream(stream)), "zero_distill_step")
 
 
 # ------------------------------------------------------------------------------ host (offload) calls

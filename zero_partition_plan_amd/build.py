@@ -24,7 +24,9 @@ CEILING_LIB = os.path.join(PKG, "libzero_ceiling.so")
 CEILING_SOURCES = [os.path.join(CSRC, "zero_ceiling.hip")]
 SOURCES = [os.path.join(CSRC, "zero_host.cpp"), os.path.join(CSRC, "zero_step.hip"),
            os.path.join(CSRC, "zero_gather.hip"), os.path.join(CSRC, "zero_host_adam.cpp"),
-           os.path.join(CSRC, "zero_offload.cpp"), os.path.join(CSRC, "zero_arena.cpp")]
+           os.path.join(CSRC, "zero_offload.cpp"), os.path.join(CSRC, "zero_arena.cpp"),
+           os.path.join(CSRC, "zero_linear.hip"), os.path.join(CSRC, "zero_gemm.hip"),
+           os.path.join(CSRC, "zero_distill.hip")]
 # the step's kernel variants, compiled once per replica / output dtype pair (zero_dtype values:
 # 0 fp32, 1 fp16, 2 bf16; an fp32 "output" means none and also carries the reduce pass)
 STEP_KERNELS = os.path.join(CSRC, "zero_step_kernels.hip")

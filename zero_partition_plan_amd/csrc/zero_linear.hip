@@ -1,0 +1,278 @@
+// The linear layer's entry points: argument checks, the pre-activation gradient and the bias
+// gradient. The products themselves are in zero_gemm.hip. ("ZeRO 优化器的三个阶段深度对比", section 三,
+// and "ZeRO：把显存“分”着用", ZeRO Stage 3: a gathered layer runs forward, and again for its backward.)
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero_act.h"
+#include "zero_internal.h"
+#include "zero_linear.h"
+
+namespace zero {
+namespace {
+
+constexpr uint64_t kMaxSize = 0x7fffffffu;
+
+// dz = round16(dy * act'(pre)), element by element.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void k_dz(const T* dy, uint64_t lddy, const T* pre, uint64_t ldp,
+                                            T* dz, uint64_t lddz, uint64_t rows, uint64_t cols) {
+  for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y)
+    for (uint64_t c = blockIdx.x * 256ull + threadIdx.x; c < cols; c += gridDim.x * 256ull)
+      dz[r * lddz + c] = (T)((float)dy[r * lddy + c] * act_slope<ACT>((float)pre[r * ldp + c]));
+}
+
+// dbias: one thread per column, rows in ascending order.
+template <typename T, typename O>
+__global__ __launch_bounds__(256) void k_db(const T* dz, uint64_t ld, uint64_t rows, uint64_t cols,
+                                            O* db, int accumulate) {
+  const uint64_t c = blockIdx.x * 256ull + threadIdx.x;
+  if (c >= cols) return;
+  float s = 0.0f;
+  for (uint64_t r = 0; r < rows; ++r) s += (float)dz[r * ld + c];
+  if (accumulate) s += (float)db[c];
+  db[c] = (O)s;
+}
+
+template <typename T>
+hipError_t run_dz(int act, const void* dy, uint64_t lddy, const void* pre, uint64_t ldp, void* dz,
+                  uint64_t lddz, uint64_t rows, uint64_t cols, hipStream_t s) {
+  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(rows < 4096 ? rows : 4096));
+#define ZERO_DZ(A)                                                                             \
+  k_dz<T, A><<<grid, dim3(256), 0, s>>>(static_cast<const T*>(dy), lddy,                       \
+                                        static_cast<const T*>(pre), ldp, static_cast<T*>(dz), \
+                                        lddz, rows, cols)
+  switch (act) {
+    case ZERO_ACT_RELU: ZERO_DZ(ZERO_ACT_RELU); break;
+    case ZERO_ACT_GELU: ZERO_DZ(ZERO_ACT_GELU); break;
+    case ZERO_ACT_GELU_TANH: ZERO_DZ(ZERO_ACT_GELU_TANH); break;
+    default: ZERO_DZ(ZERO_ACT_SILU); break;
+  }
+#undef ZERO_DZ
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t run_db(const void* dz, uint64_t ld, uint64_t rows, uint64_t cols, void* db,
+                  int accumulate, hipStream_t s) {
+  k_db<T, O><<<dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, s>>>(
+      static_cast<const T*>(dz), ld, rows, cols, static_cast<O*>(db), accumulate);
+  return hipGetLastError();
+}
+
+// One array of a call, as its checks see it.
+struct Mat {
+  const char* name;
+  const void* p;
+  uint64_t rows, cols, ld;
+  uint32_t eb;
+  bool written;
+
+  bool empty() const { return !p || rows == 0 || cols == 0; }
+  uint64_t bytes() const { return empty() ? 0 : ((rows - 1) * ld + cols) * eb; }
+};
+
+// Whether two arrays share an element. Two matrices of one leading dimension that interleave
+// without meeting (column slices of one buffer) do not.
+bool meet(const Mat& a, const Mat& b) {
+  if (!overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
+  if (a.eb != b.eb || a.rows < 2 || b.rows < 2 || a.ld != b.ld) return true;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(a.p), hi = reinterpret_cast<uintptr_t>(b.p);
+  const Mat& first = lo <= hi ? a : b;
+  const Mat& second = lo <= hi ? b : a;
+  const uint64_t d = lo <= hi ? hi - lo : lo - hi;
+  if (d % a.eb) return true;
+  const uint64_t q = d / a.eb % a.ld;  // the second's first column in the first's rows
+  return q < first.cols || q + second.cols > a.ld;
+}
+
+// Shapes and alignment of every array, then that nothing written meets anything else.
+// `same[i]` >= 0 names an array that array i may be, element for element.
+zero_status check_mats(const char* fn, Mat* m, int count, const int* same0, const int* same1) {
+  for (int i = 0; i < count; ++i) {
+    if (m[i].empty()) continue;
+    if (m[i].rows == 1) m[i].ld = m[i].cols;
+    if (m[i].ld < m[i].cols)
+      return fail(ZERO_E_INVAL, "%s: %s: leading dimension %llu below its %llu columns", fn, m[i].name,
+                  (unsigned long long)m[i].ld, (unsigned long long)m[i].cols);
+    uint64_t e;
+    if (__builtin_mul_overflow(m[i].rows, m[i].ld, &e) || e >= (1ull << 63) / 8)
+      return fail(ZERO_E_OVERFLOW, "%s: %s does not fit in 63 bits", fn, m[i].name);
+    if (reinterpret_cast<uintptr_t>(m[i].p) % m[i].eb)
+      return fail(ZERO_E_INVAL, "%s: %s is not aligned to its element size", fn, m[i].name);
+  }
+  for (int i = 0; i < count; ++i) {
+    if (!m[i].written || m[i].empty()) continue;
+    for (int j = 0; j < count; ++j) {
+      if (j == i || m[j].empty() || (m[j].written && j < i)) continue;
+      if ((same0[i] == j || same1[i] == j) && m[i].p == m[j].p && m[i].ld == m[j].ld) continue;
+      if (meet(m[i], m[j]))
+        return fail(ZERO_E_INVAL, "%s: %s overlaps %s", fn, m[i].name, m[j].name);
+    }
+  }
+  return ZERO_OK;
+}
+
+zero_status check_shape(const char* fn, const zero_linear_shape* s) {
+  if (!s) return fail(ZERO_E_INVAL, "%s: shape is NULL", fn);
+  if (!dtype_valid(s->dtype)) return fail(ZERO_E_INVAL, "%s: unknown dtype %d", fn, s->dtype);
+  if (s->dtype == ZERO_F32)
+    return fail(ZERO_E_UNSUPPORTED, "%s: dtype must be bf16 or fp16", fn);
+  if (s->act < ZERO_ACT_NONE || s->act > ZERO_ACT_SILU)
+    return fail(ZERO_E_INVAL, "%s: unknown activation %d", fn, s->act);
+  if (s->rows > kMaxSize || s->in_features > kMaxSize || s->out_features > kMaxSize)
+    return fail(ZERO_E_OVERFLOW, "%s: a size above 2^31 - 1", fn);
+  return ZERO_OK;
+}
+
+zero_status check_workspace(const char* fn, const zero_linear_shape* s, bool backward, void* ws,
+                            uint64_t bytes) {
+  const uint64_t need =
+      zero_linear_workspace_bytes(s->rows, s->in_features, s->out_features, backward);
+  if (need == 0) return ZERO_OK;
+  if (!ws || bytes < need)
+    return fail(ZERO_E_INVAL, "%s: workspace of %llu bytes, %llu needed", fn,
+                (unsigned long long)(ws ? bytes : 0), (unsigned long long)need);
+  if (reinterpret_cast<uintptr_t>(ws) % 16)
+    return fail(ZERO_E_INVAL, "%s: workspace is not aligned to 16 bytes", fn);
+  return ZERO_OK;
+}
+
+zero_status hip_result(const char* fn, hipError_t e) {
+  if (e != hipSuccess) return fail(ZERO_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return ok();
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+uint64_t zero_linear_workspace_bytes(uint64_t rows, uint64_t in_features, uint64_t out_features,
+                                     int32_t backward) {
+  if (rows > kMaxSize || in_features > kMaxSize || out_features > kMaxSize) return 0;
+  if (!backward) return gemm_workspace_bytes(rows, out_features, in_features);
+  const uint64_t dx = gemm_workspace_bytes(rows, in_features, out_features);
+  const uint64_t dw = gemm_workspace_bytes(out_features, in_features, rows);
+  return dx > dw ? dx : dw;
+}
+
+zero_status zero_linear_forward(const zero_linear_shape* s, const void* x, uint64_t ldx,
+                                const void* weight, const void* bias, const void* residual,
+                                uint64_t ldr, void* pre, uint64_t ldp, void* y, uint64_t ldy,
+                                void* workspace, uint64_t workspace_bytes, void* stream) {
+  const char* fn = "zero_linear_forward";
+  if (zero_status st = check_shape(fn, s)) return st;
+  const uint64_t M = s->rows, K = s->in_features, N = s->out_features;
+  if (M == 0 || N == 0) return ok();
+  if (!y) return fail(ZERO_E_INVAL, "%s: y is NULL", fn);
+  if (K && (!x || !weight)) return fail(ZERO_E_INVAL, "%s: x or weight is NULL", fn);
+  if (zero_status st = check_workspace(fn, s, false, workspace, workspace_bytes)) return st;
+  const uint64_t need = zero_linear_workspace_bytes(M, K, N, 0);
+  Mat m[] = {{"x", x, M, K, ldx, 2, false},
+             {"weight", weight, N, K, K, 2, false},
+             {"bias", bias, 1, N, N, 2, false},
+             {"residual", residual, M, N, ldr, 2, false},
+             {"pre", pre, M, N, ldp, 2, true},
+             {"y", y, M, N, ldy, 2, true},
+             {"workspace", need ? workspace : nullptr, 1, need, need, 1, true}};
+  const int same0[] = {-1, -1, -1, -1, -1, 3, -1}, same1[] = {-1, -1, -1, -1, -1, -1, -1};
+  if (zero_status st = check_mats(fn, m, 7, same0, same1)) return st;
+
+  (void)hipGetLastError();
+  GemmArgs g{};
+  g.a = x, g.lda = m[0].ld;
+  g.b = weight, g.ldb = K;
+  g.m = (uint32_t)M, g.n = (uint32_t)N, g.k = (uint32_t)K;
+  g.dtype = g.out_dtype = s->dtype;
+  g.act = s->act;
+  g.bias = bias;
+  g.res = residual, g.ldr = m[3].ld;
+  g.pre = pre, g.ldp = m[4].ld;
+  g.out = y, g.ldo = m[5].ld;
+  g.ws = static_cast<float*>(workspace);
+  return hip_result(fn, gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uint64_t lddy,
+                                 const void* x, uint64_t ldx, const void* weight, const void* pre,
+                                 uint64_t ldp, void* dz, uint64_t lddz, void* dx, uint64_t lddx,
+                                 void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
+                                 void* workspace, uint64_t workspace_bytes, void* stream) {
+  const char* fn = "zero_linear_backward";
+  if (zero_status st = check_shape(fn, s)) return st;
+  const uint64_t M = s->rows, K = s->in_features, N = s->out_features;
+  const bool has_act = s->act != ZERO_ACT_NONE;
+  if (!dtype_valid(grad_dtype)) return fail(ZERO_E_INVAL, "%s: unknown grad_dtype %d", fn, grad_dtype);
+  if (grad_dtype != s->dtype && grad_dtype != ZERO_F32)
+    return fail(ZERO_E_UNSUPPORTED, "%s: grad_dtype must be dtype or fp32", fn);
+  if (!has_act) pre = dz = nullptr;
+  if (!dz && !dx && !dweight && !dbias && M && N)
+    return fail(ZERO_E_INVAL, "%s: no output requested", fn);
+  if (M && N) {
+    if (!dy) return fail(ZERO_E_INVAL, "%s: dy is NULL", fn);
+    if (has_act && (!pre || !dz)) return fail(ZERO_E_INVAL, "%s: pre or dz is NULL", fn);
+    if (K && dweight && !x) return fail(ZERO_E_INVAL, "%s: x is NULL", fn);
+    if (K && dx && !weight) return fail(ZERO_E_INVAL, "%s: weight is NULL", fn);
+  }
+  if (zero_status st = check_workspace(fn, s, true, workspace, workspace_bytes)) return st;
+  const uint64_t need = zero_linear_workspace_bytes(M, K, N, 1);
+  const uint32_t gb = dtype_bytes(grad_dtype);
+  Mat m[] = {{"dy", dy, M, N, lddy, 2, false},
+             {"x", x, M, K, ldx, 2, false},
+             {"weight", weight, N, K, K, 2, false},
+             {"pre", pre, M, N, ldp, 2, false},
+             {"dz", dz, M, N, lddz, 2, true},
+             {"dx", dx, M, K, lddx, 2, true},
+             {"dweight", dweight, N, K, K, gb, true},
+             {"dbias", dbias, 1, N, N, gb, true},
+             {"workspace", need ? workspace : nullptr, 1, need, need, 1, true}};
+  const int same0[] = {-1, -1, -1, -1, 0, -1, -1, -1, -1};
+  const int same1[] = {-1, -1, -1, -1, 3, -1, -1, -1, -1};
+  if (zero_status st = check_mats(fn, m, 9, same0, same1)) return st;
+
+  hipStream_t strm = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  hipError_t e = hipSuccess;
+  const bool bf = s->dtype == ZERO_BF16;
+  const void* d = dy;
+  uint64_t ldd = m[0].ld;
+  if (has_act && M && N) {
+    e = bf ? run_dz<__bf16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, strm)
+           : run_dz<_Float16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, strm);
+    d = dz, ldd = m[4].ld;
+  }
+  if (e == hipSuccess && dx && M && K) {
+    GemmArgs g{};
+    g.a = d, g.lda = ldd;
+    g.b = weight, g.ldb = K, g.b_kmajor = true;
+    g.m = (uint32_t)M, g.n = (uint32_t)K, g.k = (uint32_t)N;
+    g.dtype = g.out_dtype = s->dtype;
+    g.out = dx, g.ldo = m[5].ld;
+    g.ws = static_cast<float*>(workspace);
+    e = gemm(g, strm);
+  }
+  if (e == hipSuccess && dweight && N && K && !(M == 0 && accumulate)) {
+    GemmArgs g{};
+    g.a = d, g.lda = ldd, g.a_kmajor = true;
+    g.b = x, g.ldb = m[1].ld, g.b_kmajor = true;
+    g.m = (uint32_t)N, g.n = (uint32_t)K, g.k = (uint32_t)M;
+    g.dtype = s->dtype, g.out_dtype = grad_dtype;
+    g.accumulate = accumulate != 0;
+    g.out = dweight, g.ldo = K;
+    g.ws = static_cast<float*>(workspace);
+    e = gemm(g, strm);
+  }
+  if (e == hipSuccess && dbias && N && !(M == 0 && accumulate)) {
+    const bool f32 = grad_dtype == ZERO_F32;
+    e = bf ? (f32 ? run_db<__bf16, float>(d, ldd, M, N, dbias, accumulate, strm)
+                  : run_db<__bf16, __bf16>(d, ldd, M, N, dbias, accumulate, strm))
+           : (f32 ? run_db<_Float16, float>(d, ldd, M, N, dbias, accumulate, strm)
+                  : run_db<_Float16, _Float16>(d, ldd, M, N, dbias, accumulate, strm));
+  }
+  return hip_result(fn, e);
+}
+
+}  // extern "C"
