@@ -28,6 +28,7 @@ class Placed:
     the rest filled with a canary that must survive."""
 
     def __init__(self, rows, cols, dtype, off=0, pad=0, fill=-77.0):
+        pad = 16 - cols % 8 if pad == "to 8" else pad
         self.rows, self.cols, self.ld, self.off, self.fill = rows, cols, cols + pad, off, fill
         self.buf = torch.full((off + rows * self.ld + 9,), fill, dtype=dtype, device=DEV)
         self.t = self.buf[off:off + rows * self.ld].view(rows, self.ld)[:, :cols]
@@ -68,7 +69,8 @@ def same(got, want64, what):
 SIZES = [(1, 1, 1), (1, 64, 64), (2, 8, 3), (7, 33, 5), (16, 128, 64), (17, 96, 130), (1, 4096, 257), (3, 1000, 1001),
          (33, 256, 255), (64, 64, 64), (65, 72, 136), (127, 129, 128), (128, 640, 384), (200, 333, 77),
          (256, 256, 256), (257, 520, 263), (300, 2048, 40), (1000, 88, 1003), (512, 768, 512), (1030, 1024, 776)]
-PLACES = [(0, 0), (8, 8), (1, 0), (3, 5)]             # (element offset, padding of each row)
+# (element offset, padding of each row; "to 8": up to a multiple of 8 beyond the row)
+PLACES = [(0, 0), (8, 8), (1, 0), (3, 5), (8, "to 8")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

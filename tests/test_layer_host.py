@@ -85,6 +85,8 @@ def test_linear_workspace_is_checked():
         if need:
             for kw in (dict(ws=None), dict(wsb=need - 1), dict(ws=_addr(20) + 8), dict(ws=_addr(2))):
                 assert call(s, wsb=kw.pop("wsb", need), **ld, **kw) == INVAL, kw
+    for m, k, n in ((0, 5, 7), (5, 0, 7), (5, 7, 0), (0, 0, 0), (1, 1, 1)):
+        assert Z.zero_linear_workspace_bytes(m, k, n) < 1 << 20 and Z.zero_linear_workspace_bytes(m, k, n, True) < 1 << 20
     for big in ((1 << 31, 1, 1), (1, 1 << 33, 1), (1, 1, 1 << 63)):
         assert Z.zero_linear_workspace_bytes(*big) == 0 == Z.zero_linear_workspace_bytes(*big, True)
 

@@ -32,6 +32,11 @@ SOURCES = [os.path.join(CSRC, "zero_host.cpp"), os.path.join(CSRC, "zero_step.hi
 STEP_KERNELS = os.path.join(CSRC, "zero_step_kernels.hip")
 STEP_PAIRS = [(r, o) for r in (0, 1, 2) for o in (0, 1, 2)]
 
+# the matrix product's tile kernels, once per 16-bit type and operand orders (1: k-major) of a product
+# the linear layer makes: x W^T, dz W, dz^T x
+GEMM_KERNELS = os.path.join(CSRC, "zero_gemm_kernels.hip")
+GEMM_VARIANTS = [(d, a, b) for d in (1, 2) for a, b in ((0, 0), (0, 1), (1, 1))]
+
 FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-fast-math",
@@ -53,6 +58,8 @@ def _units():
     units = [(src, [], os.path.splitext(os.path.basename(src))[0]) for src in SOURCES]
     units += [(STEP_KERNELS, [f"ZERO_STEP_RDT={r}", f"ZERO_STEP_ODT={o}"], f"zero_step_kernels_{r}{o}")
               for r, o in STEP_PAIRS]
+    units += [(GEMM_KERNELS, [f"ZERO_GEMM_DT={d}", f"ZERO_GEMM_AK={a}", f"ZERO_GEMM_BK={b}"],
+               f"zero_gemm_kernels_{d}{a}{b}") for d, a, b in GEMM_VARIANTS]
     return units
 
 

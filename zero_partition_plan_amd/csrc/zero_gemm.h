@@ -1,0 +1,164 @@
+// Device side of the matrix product: what its tile kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero_act.h"
+#include "zero_linear.h"
+
+namespace zero {
+
+struct GemmDev {
+  const void *a, *b, *bias, *res;
+  void *pre, *out;
+  float* ws;            // [splits][m][n] partial sums when splits > 1
+  uint64_t lda, ldb, ldr, ldp, ldo;
+  uint32_t m, n, k;
+  uint32_t tiles_m, tiles_n, splits, k_split;
+  int32_t act, accumulate, out_f32;
+};
+
+// The tile a workgroup takes. Workgroups go round the 8 XCDs in turn, each with its own L2: each
+// XCD gets one contiguous run of tiles, and a run walks 8 tile rows at a time down the columns, so
+// that the tiles in flight on one XCD share their operands' panels.
+__device__ __forceinline__ void tile_of(const GemmDev& g, uint32_t id, uint32_t& mt, uint32_t& nt) {
+  const uint32_t total = g.tiles_m * g.tiles_n;
+  const uint32_t x = id & 7, q = total >> 3, rem = total & 7;
+  id = x * q + (x < rem ? x : rem) + (id >> 3);
+  const uint32_t group = 8 * g.tiles_n;
+  const uint32_t first = id / group * 8;
+  const uint32_t rows = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
+  const uint32_t in = id % group;
+  mt = first + in % rows;
+  nt = in / rows;
+}
+
+// Where an operand's next step begins and how many bytes lie from there to its end.
+template <typename T, bool KM>
+struct Cursor {
+  const T* p;
+  uint64_t left, ld;
+  __device__ __forceinline__ Cursor(const void* base, uint64_t ld_, uint32_t row0, uint32_t rows,
+                                    uint32_t k0, uint32_t k)
+      : ld(ld_) {
+    // elements from (row0, k0) to the operand's last
+    const uint64_t at = KM ? (uint64_t)k0 * ld + row0 : (uint64_t)row0 * ld + k0;
+    const uint64_t end = KM ? (uint64_t)(k - 1) * ld + rows : (uint64_t)(rows - 1) * ld + k;
+    p = static_cast<const T*>(base) + at;
+    left = k ? end - at : 0;
+  }
+  __device__ __forceinline__ void advance() {
+    const uint64_t by = KM ? 32 * ld : 32;
+    p += by;
+    left = left > by ? left - by : 0;
+  }
+  // in whole words: the second half of a last word belongs to no row that is used
+  __device__ __forceinline__ uint32_t bytes() const {
+    const uint64_t b = (left * 2 + 3) & ~3ull;
+    return b < 0xffffffe0ull ? (uint32_t)b : 0xffffffe0u;
+  }
+};
+
+template <typename T, bool KM, int R>
+__device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt) {
+  if constexpr (!KM) {
+    for (int row = tid; row < R; row += nt)
+      for (int k = k_left; k & 7; ++k) lds[row * 32 + (((k >> 3) ^ (row >> 1 & 3)) << 3) + (k & 7)] = (T)0.0f;
+  }
+}
+
+// z -> out for up to 8 neighbouring columns n.. of row m (fewer at the right edge). With splits the
+// partial sum goes to the workspace instead.
+template <typename T>
+__device__ __forceinline__ void finish_row(const GemmDev& g, float* z, uint64_t m, uint32_t n) {
+  typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
+  typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
+  const T* bias = static_cast<const T*>(g.bias);
+  const T* res = static_cast<const T*>(g.res);
+  T* pre = static_cast<T*>(g.pre);
+  if (n + 8 <= g.n) {
+    if (bias) {
+      const v8 b = *reinterpret_cast<const v8*>(bias + n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += (float)b[j];
+    }
+    if (pre) {
+      v8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
+      *reinterpret_cast<v8*>(pre + m * g.ldp + n) = o;
+    }
+    if (g.act) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = act_rt(z[j], g.act);
+    }
+    if (res) {
+      const v8 r = *reinterpret_cast<const v8*>(res + m * g.ldr + n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += (float)r[j];
+    }
+    if (g.out_f32) {
+      f8* out = reinterpret_cast<f8*>(static_cast<float*>(g.out) + m * g.ldo + n);
+      f8 o;
+      if (g.accumulate) {
+        o = *out;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += o[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = z[j];
+      *out = o;
+    } else {
+      v8* out = reinterpret_cast<v8*>(static_cast<T*>(g.out) + m * g.ldo + n);
+      v8 o;
+      if (g.accumulate) {
+        o = *out;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += (float)o[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
+      *out = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 7; ++j) {
+    if (n + j >= g.n) break;
+    float v = z[j];
+    if (bias) v += (float)bias[n + j];
+    if (pre) pre[m * g.ldp + n + j] = (T)v;
+    v = act_rt(v, g.act);
+    if (res) v += (float)res[m * g.ldr + n + j];
+    if (g.out_f32) {
+      float* out = static_cast<float*>(g.out) + m * g.ldo + n + j;
+      *out = g.accumulate ? v + *out : v;
+    } else {
+      T* out = static_cast<T*>(g.out) + m * g.ldo + n + j;
+      *out = (T)(g.accumulate ? v + (float)*out : v);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void finish(const GemmDev& g, float* z, uint64_t m, uint32_t n) {
+  if (g.splits > 1) {
+    typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
+    float* w = g.ws + ((uint64_t)blockIdx.y * g.m + m) * g.n + n;
+    if (n + 8 <= g.n) {
+      f8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = z[j];
+      *reinterpret_cast<f8*>(w) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (n + j < g.n) w[j] = z[j];
+    }
+    return;
+  }
+  finish_row<T>(g, z, m, n);
+}
+
+}  // namespace zero

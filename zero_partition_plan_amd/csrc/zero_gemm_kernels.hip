@@ -1,0 +1,293 @@
+// Tile kernels of the matrix product, for one 16-bit type and one pair of operand orders (set by
+// ZERO_GEMM_DT, ZERO_GEMM_AK, ZERO_GEMM_BK when this file is compiled).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero_gemm.h"
+
+#ifndef ZERO_GEMM_DT
+#define ZERO_GEMM_DT 2
+#define ZERO_GEMM_AK 0
+#define ZERO_GEMM_BK 0
+#endif
+
+namespace zero {
+namespace {
+
+#if ZERO_GEMM_DT == 2
+typedef __bf16 T;
+#else
+typedef _Float16 T;
+#endif
+constexpr bool kAK = ZERO_GEMM_AK, kBK = ZERO_GEMM_BK;
+
+typedef T t8 __attribute__((ext_vector_type(8)));
+typedef T t4 __attribute__((ext_vector_type(4)));
+typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int kStepK = 32;   // k per LDS stage
+constexpr int kStages = 4;   // LDS stages
+
+__device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
+#if ZERO_GEMM_DT == 2
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+#else
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+#endif
+}
+
+// s_waitcnt for all but the last n vector memory loads
+constexpr int vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0f70; }
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+[[maybe_unused]] __device__ __forceinline__ t4 read_tr(const T* p) {
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
+  return __builtin_bit_cast(t4, v);
+}
+
+// One operand's tile of R rows by 32 k in LDS, and how it gets there and into fragments.
+// k-contiguous operand: rows of 64 bytes, the 16-byte chunk c of row r at place c ^ (r >> 1 & 3),
+// so that 8 neighbouring rows' chunks of one k lie in 8 different 16-byte columns of the banks.
+// k-major operand: 32 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k).
+template <bool KM, int R, int NT>
+struct Tile {
+  static constexpr int kChunks = R * kStepK / 8;
+  static constexpr int kRounds = kChunks / NT;
+  static_assert(kChunks % NT == 0, "whole rounds");
+  static constexpr int kElems = R * kStepK;
+
+  static __device__ __forceinline__ int swz(int k) { return k & 3; }
+
+  // (row, k) of the chunk that lies at place q of the tile
+  static __device__ __forceinline__ void chunk_at(int q, int& row, int& k) {
+    if constexpr (!KM) {
+      row = q / 4;
+      k = ((q % 4) ^ (row >> 1 & 3)) * 8;
+    } else {
+      k = q / (R / 8);
+      const int p = q % (R / 8);
+      row = (((p >> 1) ^ swz(k)) << 4) + (p & 1) * 8;
+    }
+  }
+
+  uint32_t voff[kRounds];
+  int k0;  // the first k of this thread's chunks (k-contiguous: the same in every round)
+
+  __device__ __forceinline__ void init(uint64_t ld, int tid) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      int row, k;
+      chunk_at(r * NT + tid, row, k);
+      voff[r] = (uint32_t)((KM ? (uint64_t)k * ld + row : (uint64_t)row * ld + k) * 2);
+      k0 = k;
+    }
+  }
+
+  // Straight to LDS: `base` is the address of (first row, first k of this step), `bytes` what
+  // lies behind it; a load past that gives 0. k_left: k from the step's first to the end.
+  __device__ __forceinline__ void dma(const T* base, uint32_t bytes, int k_left, T* lds, int wave) const {
+    auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
+    const bool past = !KM && k0 >= k_left;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (r * NT + wave * 64) * 8), 16,
+          past ? 0xfffffff0u : voff[r], 0, 0, 0);
+  }
+
+  // Fragment for 32 rows from row0 and 16 k from kk*16, read from LDS.
+  static __device__ __forceinline__ t8 frag(const T* lds, int row0, int kk, int lane) {
+    if constexpr (!KM) {
+      const int row = row0 + (lane & 31);
+      const int c = (kk * 2 + (lane >> 5)) ^ (lane >> 1 & 3);
+      return *reinterpret_cast<const t8*>(lds + row * kStepK + c * 8);
+    } else {
+      const int g = lane >> 4, i = lane & 15;
+      const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
+      const int gran = (row0 >> 4) + (g & 1);
+      const T* p = lds + k * R + ((gran ^ swz(k)) << 4) + (i & 3) * 4;
+      const t4 lo = read_tr(p), hi = read_tr(p + 4 * R);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+template <int BM, int BN, int WM, int WN>
+struct Shape {
+  static constexpr int NT = WM * WN * 64;
+  static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  using A = Tile<kAK, BM, NT>;
+  using B = Tile<kBK, BN, NT>;
+  static constexpr int kStage = A::kElems + B::kElems;
+};
+
+template <typename S>
+struct Frags {
+  t8 a[S::TM], b[S::TN];
+  __device__ __forceinline__ void load(const T* stage, int kk, int wm0, int wn0, int lane) {
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) b[j] = S::B::frag(stage + S::A::kElems, wn0 + j * 32, kk, lane);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) a[i] = S::A::frag(stage, wm0 + i * 32, kk, lane);
+  }
+  __device__ __forceinline__ void mul(f16v (&acc)[S::TM][S::TN]) const {
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) acc[i][j] = mfma(b[j], a[i], acc[i][j]);
+  }
+};
+
+// One step: the loads of step s + 3 on their way into `dst`, the products of `cur`, and the first
+// fragments of `next`. The buffers are declared apart, so that the reads of one need not wait for
+// what is on its way into another.
+template <typename S>
+__device__ __forceinline__ void step(const T* __restrict__ cur, const T* __restrict__ next,
+                                     T* __restrict__ dst, const typename S::A& ta, const typename S::B& tb,
+                                     const T* pa, uint32_t abytes, const T* pb, uint32_t bbytes, int k_left,
+                                     Frags<S>& f, f16v (&acc)[S::TM][S::TN], int wm0, int wn0, int wave,
+                                     int lane) {
+  Frags<S> h;
+  ta.dma(pa, abytes, k_left, dst, wave);
+  tb.dma(pb, bbytes, k_left, dst + S::A::kElems, wave);
+  h.load(cur, 1, wm0, wn0, lane);
+  f.mul(acc);
+  f.load(next, 0, wm0, wn0, lane);
+  h.mul(acc);
+  // one load or LDS read behind each matrix instruction
+  constexpr int reads = (S::TM * (kAK ? 2 : 1) + S::TN * (kBK ? 2 : 1));
+  constexpr int muls = S::TM * S::TN;
+  constexpr int per = (reads + muls - 1) / muls;
+#pragma unroll
+  for (int i = 0; i < muls; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < muls; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+  }
+}
+
+template <typename S, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  T* lds = reinterpret_cast<T*>(smem);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  uint32_t mt, nt;
+  tile_of(g, blockIdx.x, mt, nt);
+  const uint32_t m0 = mt * BM, n0 = nt * BN;
+  const uint32_t k_begin = blockIdx.y * g.k_split;
+  const uint32_t k_end = k_begin + g.k_split < g.k ? k_begin + g.k_split : g.k;
+  const int wm0 = (wave / WN) * (BM / WM), wn0 = (wave % WN) * (BN / WN);
+
+  typename S::A ta;
+  typename S::B tb;
+  ta.init(g.lda, tid);
+  tb.init(g.ldb, tid);
+  Cursor<T, kAK> ca(g.a, g.lda, m0, g.m, k_begin, g.k);
+  Cursor<T, kBK> cb(g.b, g.ldb, n0, g.n, k_begin, g.k);
+
+  f16v acc[S::TM][S::TN] = {};
+  const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
+  int k_left = (int)(g.k - k_begin);
+  constexpr int kLoads = S::A::kRounds + S::B::kRounds;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    ta.dma(ca.p, ca.bytes(), k_left, lds + s * S::kStage, wave);
+    tb.dma(cb.p, cb.bytes(), k_left, lds + s * S::kStage + S::A::kElems, wave);
+    ca.advance();
+    cb.advance();
+    k_left -= kStepK;
+  }
+  // k's last, partial chunk of a k-contiguous row comes with what lies behind the row
+  const int part = k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
+  const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
+  __builtin_amdgcn_s_waitcnt(vmcnt(2 * kLoads));
+  __syncthreads();
+  if (part && steps == 1) {
+    zero_partial<T, kAK, BM>(lds, k_last, tid, S::NT);
+    zero_partial<T, kBK, BN>(lds + S::A::kElems, k_last, tid, S::NT);
+    __syncthreads();
+  }
+  Frags<S> f;
+  f.load(lds, 0, wm0, wn0, lane);
+  for (int s = 0; s < steps; ++s) {
+    T* next = lds + ((s + 1) & 3) * S::kStage;
+    __builtin_amdgcn_s_waitcnt(vmcnt(kLoads));
+    __syncthreads();
+    if (part && s + 2 == steps) {
+      zero_partial<T, kAK, BM>(next, k_last, tid, S::NT);
+      zero_partial<T, kBK, BN>(next + S::A::kElems, k_last, tid, S::NT);
+      __syncthreads();
+    }
+    step<S>(lds + (s & 3) * S::kStage, next, lds + ((s + 3) & 3) * S::kStage, ta, tb, ca.p, ca.bytes(), cb.p,
+            cb.bytes(), k_left, f, acc, wm0, wn0, wave, lane);
+    ca.advance();
+    cb.advance();
+    k_left -= kStepK;
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt(0));  // the last steps' loads past the end land before LDS is reused
+  __syncthreads();
+  // 32 rows at a time through LDS: the matrix instruction leaves a lane 4 neighbouring columns of
+  // one row; the epilogue wants 8 lanes on a row's 64 columns
+  float* stage = reinterpret_cast<float*>(smem) + wave * (32 * (S::TN * 32 + 4));
+  constexpr int LDSR = S::TN * 32 + 4;
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float4 v = make_float4(acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]);
+        *reinterpret_cast<float4*>(stage + (lane & 31) * LDSR + j * 32 + q * 8 + (lane >> 5) * 4) = v;
+      }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int LPR = S::TN * 32 / 8;    // lanes on a row
+    constexpr int RPP = 64 / LPR;          // rows of a pass
+    for (int r = lane / LPR; r < 32; r += RPP) {
+      const uint32_t m = m0 + wm0 + i * 32 + r, n = n0 + wn0 + (lane % LPR) * 8;
+      float z[8];
+      *reinterpret_cast<float4*>(z) = *reinterpret_cast<float4*>(stage + r * LDSR + (lane % LPR) * 8);
+      *reinterpret_cast<float4*>(z + 4) = *reinterpret_cast<float4*>(stage + r * LDSR + (lane % LPR) * 8 + 4);
+      if (m < g.m && n < g.n) finish<T>(g, z, m, n);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch(const GemmDev& g, hipStream_t s) {
+  using S = Shape<BM, BN, WM, WN>;
+  constexpr int epi = WM * WN * 32 * (S::TN * 32 + 4) * 4;
+  constexpr int lds = kStages * S::kStage * 2 > epi ? kStages * S::kStage * 2 : epi;
+  auto fn = k_gemm<S, BM, BN, WM, WN>;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  fn<<<dim3(g.tiles_m * g.tiles_n, g.splits), dim3(S::NT), lds, s>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+#define ZERO_CAT_(a, b, c, d) a##b##c##d
+#define ZERO_CAT(a, b, c, d) ZERO_CAT_(a, b, c, d)
+hipError_t ZERO_CAT(gemm_tiles_, ZERO_GEMM_DT, ZERO_GEMM_AK, ZERO_GEMM_BK)(const GemmDev& g, int shape,
+                                                                           hipStream_t s) {
+  switch (shape) {
+    case 0: return launch<256, 256, 2, 4>(g, s);
+    case 1: return launch<128, 128, 2, 2>(g, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace zero
