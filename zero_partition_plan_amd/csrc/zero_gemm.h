@@ -9,6 +9,8 @@
 
 namespace zero {
 
+constexpr uint32_t kGemmStep = 64;  // k per LDS stage; splits of k are whole stages
+
 struct GemmDev {
   const void *a, *b, *bias, *res;
   void *pre, *out;
@@ -49,7 +51,7 @@ struct Cursor {
     left = k ? end - at : 0;
   }
   __device__ __forceinline__ void advance() {
-    const uint64_t by = KM ? 32 * ld : 32;
+    const uint64_t by = KM ? kGemmStep * ld : kGemmStep;
     p += by;
     left = left > by ? left - by : 0;
   }
@@ -64,7 +66,7 @@ template <typename T, bool KM, int R>
 __device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt) {
   if constexpr (!KM) {
     for (int row = tid; row < R; row += nt)
-      for (int k = k_left; k & 7; ++k) lds[row * 32 + (((k >> 3) ^ (row >> 1 & 3)) << 3) + (k & 7)] = (T)0.0f;
+      for (int k = k_left; k & 7; ++k) lds[row * 64 + (((k >> 3) ^ (row & 7)) << 3) + (k & 7)] = (T)0.0f;
   }
 }
 

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void k_join(GemmDev g) {
 
 struct TileShape {
   uint32_t bm, bn, per_cu;
-  float cost;  // time of one 32-k step of one tile, relative
+  float cost;  // time of one step of one tile, relative
 };
 constexpr TileShape kShapes[] = {{256, 256, 1, 1.0f}, {128, 128, 2, 0.30f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
@@ -100,23 +100,23 @@ struct Plan {
 };
 
 Plan plan(uint64_t m, uint64_t n, uint64_t k) {
-  Plan best{0, 1, (uint32_t)((k + 31) / 32 * 32)};
+  Plan best{0, 1, 0};
   float best_t = 1e30f;
-  const uint64_t steps = k ? (k + 31) / 32 : 1;
-  best.k_split = (uint32_t)(steps * 32);
+  const uint64_t steps = k ? (k + kGemmStep - 1) / kGemmStep : 1;
+  best.k_split = (uint32_t)(steps * kGemmStep);
   for (int i = 0; i < kNumShapes; ++i) {
     const TileShape& t = kShapes[i];
     const uint64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
-    for (uint64_t sp = 1; sp <= 16 && (sp == 1 || steps / sp >= 8); ++sp) {
+    for (uint64_t sp = 1; sp <= 16 && (sp == 1 || steps / sp >= 4); ++sp) {
       const uint64_t per = (steps + sp - 1) / sp;
       const uint64_t slots = kCus * t.per_cu;
       const uint64_t rounds = (tiles * sp + slots - 1) / slots;
-      // k_join and the workspace's write and read, in units of a 256 x 256 x 32 step (about 1.1 us)
-      const float join = sp > 1 ? 6.0f + (float)(m * n * sp * 8) / 4e6f : 0.0f;
-      const float time = (float)(rounds * (per + 8)) * t.cost * t.per_cu + join;
+      // k_join and the workspace's write and read, in units of a 256 x 256 x 64 step (about 1.2 us)
+      const float join = sp > 1 ? 3.0f + (float)(m * n * sp * 8) / 8e6f : 0.0f;
+      const float time = (float)(rounds * (per + 4)) * t.cost * t.per_cu + join;
       if (time < best_t) {
         best_t = time;
-        best = Plan{i, (uint32_t)((steps + per - 1) / per), (uint32_t)(per * 32)};
+        best = Plan{i, (uint32_t)((steps + per - 1) / per), (uint32_t)(per * kGemmStep)};
       }
     }
   }

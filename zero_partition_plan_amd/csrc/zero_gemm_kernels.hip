@@ -26,8 +26,8 @@ typedef T t4 __attribute__((ext_vector_type(4)));
 typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kStepK = 32;   // k per LDS stage
-constexpr int kStages = 4;   // LDS stages
+constexpr int kStepK = kGemmStep;
+constexpr int kStages = 2;  // LDS stages
 
 __device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
 #if ZERO_GEMM_DT == 2
@@ -37,8 +37,8 @@ __device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
 #endif
 }
 
-// s_waitcnt for all but the last n vector memory loads
-constexpr int vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0f70; }
+// s_waitcnt for every load into LDS and every LDS access of this wave
+constexpr int kWaitAll = 0x0070;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 
@@ -48,10 +48,10 @@ typedef short s4 __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(t4, v);
 }
 
-// One operand's tile of R rows by 32 k in LDS, and how it gets there and into fragments.
-// k-contiguous operand: rows of 64 bytes, the 16-byte chunk c of row r at place c ^ (r >> 1 & 3),
-// so that 8 neighbouring rows' chunks of one k lie in 8 different 16-byte columns of the banks.
-// k-major operand: 32 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k).
+// One operand's tile of R rows by 64 k in LDS, and how it gets there and into fragments.
+// k-contiguous operand: rows of 128 bytes, the 16-byte chunk c of row r at place c ^ (r & 7), so
+// that 8 neighbouring rows' chunks of one k lie in 8 different 16-byte columns of the banks.
+// k-major operand: 64 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k).
 template <bool KM, int R, int NT>
 struct Tile {
   static constexpr int kChunks = R * kStepK / 8;
@@ -64,8 +64,8 @@ struct Tile {
   // (row, k) of the chunk that lies at place q of the tile
   static __device__ __forceinline__ void chunk_at(int q, int& row, int& k) {
     if constexpr (!KM) {
-      row = q / 4;
-      k = ((q % 4) ^ (row >> 1 & 3)) * 8;
+      row = q / 8;
+      k = ((q % 8) ^ (row & 7)) * 8;
     } else {
       k = q / (R / 8);
       const int p = q % (R / 8);
@@ -102,7 +102,7 @@ struct Tile {
   static __device__ __forceinline__ t8 frag(const T* lds, int row0, int kk, int lane) {
     if constexpr (!KM) {
       const int row = row0 + (lane & 31);
-      const int c = (kk * 2 + (lane >> 5)) ^ (lane >> 1 & 3);
+      const int c = (kk * 2 + (lane >> 5)) ^ (lane & 7);
       return *reinterpret_cast<const t8*>(lds + row * kStepK + c * 8);
     } else {
       const int g = lane >> 4, i = lane & 15;
@@ -141,34 +141,40 @@ struct Frags {
   }
 };
 
-// One step: the loads of step s + 3 on their way into `dst`, the products of `cur`, and the first
-// fragments of `next`. The buffers are declared apart, so that the reads of one need not wait for
-// what is on its way into another.
+// From the last quarter of one step to the third of the next. On entry f holds the last
+// fragments of the stage in `dst`, which no wave reads any more: the loads of the step after
+// the next go there, while the products run through `cur`. The buffers are declared apart, so that
+// the reads of one need not wait for what is on its way into the other.
 template <typename S>
-__device__ __forceinline__ void step(const T* __restrict__ cur, const T* __restrict__ next,
-                                     T* __restrict__ dst, const typename S::A& ta, const typename S::B& tb,
-                                     const T* pa, uint32_t abytes, const T* pb, uint32_t bbytes, int k_left,
+__device__ __forceinline__ void step(const T* __restrict__ cur, T* __restrict__ dst,
+                                     const typename S::A& ta, const typename S::B& tb, const T* pa,
+                                     uint32_t abytes, const T* pb, uint32_t bbytes, int k_left,
                                      Frags<S>& f, f16v (&acc)[S::TM][S::TN], int wm0, int wn0, int wave,
                                      int lane) {
   Frags<S> h;
   ta.dma(pa, abytes, k_left, dst, wave);
   tb.dma(pb, bbytes, k_left, dst + S::A::kElems, wave);
-  h.load(cur, 1, wm0, wn0, lane);
+  h.load(cur, 0, wm0, wn0, lane);
   f.mul(acc);
-  f.load(next, 0, wm0, wn0, lane);
+  f.load(cur, 1, wm0, wn0, lane);
   h.mul(acc);
-  // one load or LDS read behind each matrix instruction
+  h.load(cur, 2, wm0, wn0, lane);
+  f.mul(acc);
+  f.load(cur, 3, wm0, wn0, lane);
+  h.mul(acc);
+  // behind each matrix instruction its share of the LDS reads of the next quarter, and of the loads
   constexpr int reads = (S::TM * (kAK ? 2 : 1) + S::TN * (kBK ? 2 : 1));
   constexpr int muls = S::TM * S::TN;
   constexpr int per = (reads + muls - 1) / muls;
+  constexpr int loads = (S::A::kRounds + S::B::kRounds + muls - 1) / muls;
 #pragma unroll
   for (int i = 0; i < muls; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
-    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x20, loads, 0);
   }
 #pragma unroll
-  for (int i = 0; i < muls; ++i) {
+  for (int i = 0; i < 3 * muls; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
   }
@@ -197,43 +203,33 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   f16v acc[S::TM][S::TN] = {};
   const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
   int k_left = (int)(g.k - k_begin);
-  constexpr int kLoads = S::A::kRounds + S::B::kRounds;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    ta.dma(ca.p, ca.bytes(), k_left, lds + s * S::kStage, wave);
-    tb.dma(cb.p, cb.bytes(), k_left, lds + s * S::kStage + S::A::kElems, wave);
-    ca.advance();
-    cb.advance();
-    k_left -= kStepK;
-  }
   // k's last, partial chunk of a k-contiguous row comes with what lies behind the row
   const int part = k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
   const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
-  __builtin_amdgcn_s_waitcnt(vmcnt(2 * kLoads));
-  __syncthreads();
-  if (part && steps == 1) {
-    zero_partial<T, kAK, BM>(lds, k_last, tid, S::NT);
-    zero_partial<T, kBK, BN>(lds + S::A::kElems, k_last, tid, S::NT);
-    __syncthreads();
+  Frags<S> f = {};
+  if (steps > 0) {
+    ta.dma(ca.p, ca.bytes(), k_left, lds, wave);
+    tb.dma(cb.p, cb.bytes(), k_left, lds + S::A::kElems, wave);
   }
-  Frags<S> f;
-  f.load(lds, 0, wm0, wn0, lane);
   for (int s = 0; s < steps; ++s) {
-    T* next = lds + ((s + 1) & 3) * S::kStage;
-    __builtin_amdgcn_s_waitcnt(vmcnt(kLoads));
+    T* cur = lds + (s & 1) * S::kStage;
+    // what the next stage needs has landed, and this wave's reads of the stage that is to be loaded
+    // over are done: the barrier makes both true of all waves
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
     __syncthreads();
-    if (part && s + 2 == steps) {
-      zero_partial<T, kAK, BM>(next, k_last, tid, S::NT);
-      zero_partial<T, kBK, BN>(next + S::A::kElems, k_last, tid, S::NT);
+    if (part && s + 1 == steps) {
+      zero_partial<T, kAK, BM>(cur, k_last, tid, S::NT);
+      zero_partial<T, kBK, BN>(cur + S::A::kElems, k_last, tid, S::NT);
       __syncthreads();
     }
-    step<S>(lds + (s & 3) * S::kStage, next, lds + ((s + 3) & 3) * S::kStage, ta, tb, ca.p, ca.bytes(), cb.p,
-            cb.bytes(), k_left, f, acc, wm0, wn0, wave, lane);
     ca.advance();
     cb.advance();
     k_left -= kStepK;
+    step<S>(cur, lds + (~s & 1) * S::kStage, ta, tb, ca.p, ca.bytes(), cb.p, cb.bytes(), k_left, f, acc,
+            wm0, wn0, wave, lane);
   }
-  __builtin_amdgcn_s_waitcnt(vmcnt(0));  // the last steps' loads past the end land before LDS is reused
+  f.mul(acc);
+  __builtin_amdgcn_s_waitcnt(kWaitAll);  // the last step's loads past the end land before LDS is reused
   __syncthreads();
   // 32 rows at a time through LDS: the matrix instruction leaves a lane 4 neighbouring columns of
   // one row; the epilogue wants 8 lanes on a row's 64 columns
