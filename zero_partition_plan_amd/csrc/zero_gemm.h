@@ -36,29 +36,29 @@ __device__ __forceinline__ void tile_of(const GemmDev& g, uint32_t id, uint32_t&
   nt = in / rows;
 }
 
-// Where an operand's next step begins and how many bytes lie from there to its end.
-template <typename T, bool KM>
+// Where an operand's next step begins, and the bytes from there to the last element that the tile
+// uses of it: what the loads are checked against. Everything but the address fits in 32 bits, as a
+// tile spans at most 256 rows of at most 2^22 elements. Sizes are rounded up to whole words, the
+// second half of a last word belonging to no row that is used.
+template <typename T, bool KM, int R>
 struct Cursor {
   const T* p;
-  uint64_t left, ld;
-  __device__ __forceinline__ Cursor(const void* base, uint64_t ld_, uint32_t row0, uint32_t rows,
-                                    uint32_t k0, uint32_t k)
-      : ld(ld_) {
-    // elements from (row0, k0) to the operand's last
-    const uint64_t at = KM ? (uint64_t)k0 * ld + row0 : (uint64_t)row0 * ld + k0;
-    const uint64_t end = KM ? (uint64_t)(k - 1) * ld + rows : (uint64_t)(rows - 1) * ld + k;
-    p = static_cast<const T*>(base) + at;
-    left = k ? end - at : 0;
+  uint32_t fixed, ld2;
+  uint64_t by;
+  __device__ __forceinline__ Cursor(const void* base, uint64_t ld, uint32_t row0, uint32_t rows,
+                                    uint32_t k0) {
+    p = static_cast<const T*>(base) + (KM ? (uint64_t)k0 * ld + row0 : (uint64_t)row0 * ld + k0);
+    const uint32_t here = rows - row0 < R ? rows - row0 : R;
+    fixed = KM ? (here * 2 + 3) & ~3u : (here - 1) * (uint32_t)ld * 2;
+    ld2 = (uint32_t)ld * 2;
+    by = KM ? kGemmStep * ld : kGemmStep;
   }
-  __device__ __forceinline__ void advance() {
-    const uint64_t by = KM ? kGemmStep * ld : kGemmStep;
-    p += by;
-    left = left > by ? left - by : 0;
-  }
-  // in whole words: the second half of a last word belongs to no row that is used
-  __device__ __forceinline__ uint32_t bytes() const {
-    const uint64_t b = (left * 2 + 3) & ~3ull;
-    return b < 0xffffffe0ull ? (uint32_t)b : 0xffffffe0u;
+  __device__ __forceinline__ void advance() { p += by; }
+  // k_left: k from the step's first to the operand's end
+  __device__ __forceinline__ uint32_t bytes(int k_left) const {
+    if (k_left <= 0) return 0;
+    if (KM) return fixed + ((k_left < (int)kGemmStep ? k_left : (int)kGemmStep) - 1) * ld2;
+    return fixed + (((uint32_t)k_left * 2 + 3) & ~3u);
   }
 };
 
@@ -66,7 +66,7 @@ template <typename T, bool KM, int R>
 __device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt) {
   if constexpr (!KM) {
     for (int row = tid; row < R; row += nt)
-      for (int k = k_left; k & 7; ++k) lds[row * 64 + (((k >> 3) ^ (row & 7)) << 3) + (k & 7)] = (T)0.0f;
+      for (int k = k_left; k & 7; ++k) lds[row * 64 + (((k >> 3) ^ (row >> 1 & 7)) << 3) + (k & 7)] = (T)0.0f;
   }
 }
 

@@ -37,6 +37,11 @@ __device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
 #endif
 }
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
 // s_waitcnt for every load into LDS and every LDS access of this wave
 constexpr int kWaitAll = 0x0070;
 
@@ -49,9 +54,11 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 }
 
 // One operand's tile of R rows by 64 k in LDS, and how it gets there and into fragments.
-// k-contiguous operand: rows of 128 bytes, the 16-byte chunk c of row r at place c ^ (r & 7), so
-// that 8 neighbouring rows' chunks of one k lie in 8 different 16-byte columns of the banks.
-// k-major operand: 64 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k).
+// k-contiguous operand: rows of 128 bytes, the 16-byte chunk c of row r at place c ^ (r >> 1 & 7):
+// the LDS answers 16 lanes of a 16-byte read at once from 256 bytes of banks, and 16 neighbouring
+// rows' chunks of one k then lie in its 16 different places.
+// k-major operand: 64 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k): a
+// transposing read takes 32 lanes at once, 4 k of 2 neighbouring granules, again 256 bytes apart.
 template <bool KM, int R, int NT>
 struct Tile {
   static constexpr int kChunks = R * kStepK / 8;
@@ -59,13 +66,13 @@ struct Tile {
   static_assert(kChunks % NT == 0, "whole rounds");
   static constexpr int kElems = R * kStepK;
 
-  static __device__ __forceinline__ int swz(int k) { return k & 3; }
+  static __device__ __forceinline__ int swz(int k) { return R % 128 == 0 ? (k & 3) << 1 : k & 2; }
 
   // (row, k) of the chunk that lies at place q of the tile
   static __device__ __forceinline__ void chunk_at(int q, int& row, int& k) {
     if constexpr (!KM) {
       row = q / 8;
-      k = ((q % 8) ^ (row & 7)) * 8;
+      k = ((q % 8) ^ (row >> 1 & 7)) * 8;
     } else {
       k = q / (R / 8);
       const int p = q % (R / 8);
@@ -102,7 +109,7 @@ struct Tile {
   static __device__ __forceinline__ t8 frag(const T* lds, int row0, int kk, int lane) {
     if constexpr (!KM) {
       const int row = row0 + (lane & 31);
-      const int c = (kk * 2 + (lane >> 5)) ^ (lane & 7);
+      const int c = (kk * 2 + (lane >> 5)) ^ (lane >> 1 & 7);
       return *reinterpret_cast<const t8*>(lds + row * kStepK + c * 8);
     } else {
       const int g = lane >> 4, i = lane & 15;
@@ -115,23 +122,26 @@ struct Tile {
   }
 };
 
+// Stages of one operand lie side by side, A's before B's: the reads of both stages are then
+// immediate offsets from the same addresses.
 template <int BM, int BN, int WM, int WN>
 struct Shape {
   static constexpr int NT = WM * WN * 64;
   static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   using A = Tile<kAK, BM, NT>;
   using B = Tile<kBK, BN, NT>;
-  static constexpr int kStage = A::kElems + B::kElems;
+  static constexpr int kB = kStages * A::kElems;
+  static constexpr int kElems = kB + kStages * B::kElems;
 };
 
 template <typename S>
 struct Frags {
   t8 a[S::TM], b[S::TN];
-  __device__ __forceinline__ void load(const T* stage, int kk, int wm0, int wn0, int lane) {
+  __device__ __forceinline__ void load(const T* sa, const T* sb, int kk, int wm0, int wn0, int lane) {
 #pragma unroll
-    for (int j = 0; j < S::TN; ++j) b[j] = S::B::frag(stage + S::A::kElems, wn0 + j * 32, kk, lane);
+    for (int j = 0; j < S::TN; ++j) b[j] = S::B::frag(sb, wn0 + j * 32, kk, lane);
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i) a[i] = S::A::frag(stage, wm0 + i * 32, kk, lane);
+    for (int i = 0; i < S::TM; ++i) a[i] = S::A::frag(sa, wm0 + i * 32, kk, lane);
   }
   __device__ __forceinline__ void mul(f16v (&acc)[S::TM][S::TN]) const {
 #pragma unroll
@@ -142,25 +152,25 @@ struct Frags {
 };
 
 // From the last quarter of one step to the third of the next. On entry f holds the last
-// fragments of the stage in `dst`, which no wave reads any more: the loads of the step after
-// the next go there, while the products run through `cur`. The buffers are declared apart, so that
-// the reads of one need not wait for what is on its way into the other.
+// fragments of the stage at da and db, which no wave reads any more: the loads of the step after
+// the next go there, while the products run through the stage at sa and sb. The stages are declared
+// apart, so that the reads of one need not wait for what is on its way into the other.
 template <typename S>
-__device__ __forceinline__ void step(const T* __restrict__ cur, T* __restrict__ dst,
-                                     const typename S::A& ta, const typename S::B& tb, const T* pa,
-                                     uint32_t abytes, const T* pb, uint32_t bbytes, int k_left,
-                                     Frags<S>& f, f16v (&acc)[S::TM][S::TN], int wm0, int wn0, int wave,
-                                     int lane) {
+__device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restrict__ sb,
+                                     T* __restrict__ da, T* __restrict__ db, const typename S::A& ta,
+                                     const typename S::B& tb, const T* pa, uint32_t abytes, const T* pb,
+                                     uint32_t bbytes, int k_left, Frags<S>& f, f16v (&acc)[S::TM][S::TN],
+                                     int wm0, int wn0, int wave, int lane) {
   Frags<S> h;
-  ta.dma(pa, abytes, k_left, dst, wave);
-  tb.dma(pb, bbytes, k_left, dst + S::A::kElems, wave);
-  h.load(cur, 0, wm0, wn0, lane);
+  ta.dma(pa, abytes, k_left, da, wave);
+  tb.dma(pb, bbytes, k_left, db, wave);
+  h.load(sa, sb, 0, wm0, wn0, lane);
   f.mul(acc);
-  f.load(cur, 1, wm0, wn0, lane);
+  f.load(sa, sb, 1, wm0, wn0, lane);
   h.mul(acc);
-  h.load(cur, 2, wm0, wn0, lane);
+  h.load(sa, sb, 2, wm0, wn0, lane);
   f.mul(acc);
-  f.load(cur, 3, wm0, wn0, lane);
+  f.load(sa, sb, 3, wm0, wn0, lane);
   h.mul(acc);
   // behind each matrix instruction its share of the LDS reads of the next quarter, and of the loads
   constexpr int reads = (S::TM * (kAK ? 2 : 1) + S::TN * (kBK ? 2 : 1));
@@ -197,8 +207,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   typename S::B tb;
   ta.init(g.lda, tid);
   tb.init(g.ldb, tid);
-  Cursor<T, kAK> ca(g.a, g.lda, m0, g.m, k_begin, g.k);
-  Cursor<T, kBK> cb(g.b, g.ldb, n0, g.n, k_begin, g.k);
+  Cursor<T, kAK, BM> ca(g.a, g.lda, m0, g.m, k_begin);
+  Cursor<T, kBK, BN> cb(g.b, g.ldb, n0, g.n, k_begin);
 
   f16v acc[S::TM][S::TN] = {};
   const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
@@ -208,25 +218,31 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
   Frags<S> f = {};
   if (steps > 0) {
-    ta.dma(ca.p, ca.bytes(), k_left, lds, wave);
-    tb.dma(cb.p, cb.bytes(), k_left, lds + S::A::kElems, wave);
+    ta.dma(ca.p, ca.bytes(k_left), k_left, lds, wave);
+    tb.dma(cb.p, cb.bytes(k_left), k_left, lds + S::kB, wave);
   }
-  for (int s = 0; s < steps; ++s) {
-    T* cur = lds + (s & 1) * S::kStage;
+  auto body = [&](auto parity, bool last) {
+    constexpr int P = decltype(parity)::value;
+    T *sa = lds + P * S::A::kElems, *sb = lds + S::kB + P * S::B::kElems;
+    ca.advance();
+    cb.advance();
+    k_left -= kStepK;
+    const uint32_t abytes = ca.bytes(k_left), bbytes = cb.bytes(k_left);
     // what the next stage needs has landed, and this wave's reads of the stage that is to be loaded
     // over are done: the barrier makes both true of all waves
     __builtin_amdgcn_s_waitcnt(kWaitAll);
     __syncthreads();
-    if (part && s + 1 == steps) {
-      zero_partial<T, kAK, BM>(cur, k_last, tid, S::NT);
-      zero_partial<T, kBK, BN>(cur + S::A::kElems, k_last, tid, S::NT);
+    if (part && last) {
+      zero_partial<T, kAK, BM>(sa, k_last, tid, S::NT);
+      zero_partial<T, kBK, BN>(sb, k_last, tid, S::NT);
       __syncthreads();
     }
-    ca.advance();
-    cb.advance();
-    k_left -= kStepK;
-    step<S>(cur, lds + (~s & 1) * S::kStage, ta, tb, ca.p, ca.bytes(), cb.p, cb.bytes(), k_left, f, acc,
-            wm0, wn0, wave, lane);
+    step<S>(sa, sb, lds + (1 - P) * S::A::kElems, lds + S::kB + (1 - P) * S::B::kElems, ta, tb, ca.p,
+            abytes, cb.p, bbytes, k_left, f, acc, wm0, wn0, wave, lane);
+  };
+  for (int s = 0; s < steps; s += 2) {
+    body(Int<0>{}, s + 1 == steps);
+    if (s + 1 < steps) body(Int<1>{}, s + 2 == steps);
   }
   f.mul(acc);
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // the last step's loads past the end land before LDS is reused
@@ -262,7 +278,7 @@ template <int BM, int BN, int WM, int WN>
 hipError_t launch(const GemmDev& g, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
   constexpr int epi = WM * WN * 32 * (S::TN * 32 + 4) * 4;
-  constexpr int lds = kStages * S::kStage * 2 > epi ? kStages * S::kStage * 2 : epi;
+  constexpr int lds = S::kElems * 2 > epi ? S::kElems * 2 : epi;
   auto fn = k_gemm<S, BM, BN, WM, WN>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
