@@ -52,15 +52,22 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.0f;
 }
 
-// The activation chosen at run time (uniform over the launch): the five differ in a few
-// instructions per element, which the product in front of them hides.
-__device__ __forceinline__ float act_rt(float z, int a) {
+// The activation chosen at run time (uniform over the launch), for N values at once: one branch, and
+// each activation's code once per kernel.
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float* z) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) z[j] = act<ACT>(z[j]);
+}
+
+template <int N>
+__device__ __forceinline__ void act_rt(float* z, int a) {
   switch (a) {
-    case ZERO_ACT_RELU: return act<ZERO_ACT_RELU>(z);
-    case ZERO_ACT_GELU: return act<ZERO_ACT_GELU>(z);
-    case ZERO_ACT_GELU_TANH: return act<ZERO_ACT_GELU_TANH>(z);
-    case ZERO_ACT_SILU: return act<ZERO_ACT_SILU>(z);
-    default: return z;
+    case ZERO_ACT_RELU: act_all<ZERO_ACT_RELU, N>(z); break;
+    case ZERO_ACT_GELU: act_all<ZERO_ACT_GELU, N>(z); break;
+    case ZERO_ACT_GELU_TANH: act_all<ZERO_ACT_GELU_TANH, N>(z); break;
+    case ZERO_ACT_SILU: act_all<ZERO_ACT_SILU, N>(z); break;
+    default: break;
   }
 }
 

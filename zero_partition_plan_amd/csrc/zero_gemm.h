@@ -11,6 +11,16 @@ namespace zero {
 
 constexpr uint32_t kGemmStep = 64;  // k per LDS stage; splits of k are whole stages
 
+// Tile shapes: rows, columns, waves along the rows, waves along the columns.
+#define ZERO_GEMM_SHAPES        \
+  ZERO_SHAPE(0, 256, 256, 2, 4) \
+  ZERO_SHAPE(1, 128, 256, 2, 4) \
+  ZERO_SHAPE(2, 256, 128, 4, 2) \
+  ZERO_SHAPE(3, 128, 128, 2, 2) \
+  ZERO_SHAPE(4, 64, 256, 1, 4)  \
+  ZERO_SHAPE(5, 32, 256, 1, 4)  \
+  ZERO_SHAPE(6, 64, 64, 2, 2)
+
 struct GemmDev {
   const void *a, *b, *bias, *res;
   void *pre, *out;
@@ -70,75 +80,71 @@ __device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt
   }
 }
 
-// z -> out for up to 8 neighbouring columns n.. of row m (fewer at the right edge). With splits the
-// partial sum goes to the workspace instead.
+// z -> out for up to 8 neighbouring columns n.. of row m (fewer at the right edge). The activation
+// stands once for both kinds of row; vectors may lie at any element.
 template <typename T>
 __device__ __forceinline__ void finish_row(const GemmDev& g, float* z, uint64_t m, uint32_t n) {
   typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
   typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
-  const T* bias = static_cast<const T*>(g.bias);
-  const T* res = static_cast<const T*>(g.res);
-  T* pre = static_cast<T*>(g.pre);
+  const T* bias = static_cast<const T*>(g.bias) + n;
+  const T* res = static_cast<const T*>(g.res) + m * g.ldr + n;
+  T* pre = static_cast<T*>(g.pre) + m * g.ldp + n;
+  float* out32 = static_cast<float*>(g.out) + m * g.ldo + n;
+  T* out16 = static_cast<T*>(g.out) + m * g.ldo + n;
   if (n + 8 <= g.n) {
-    if (bias) {
-      const v8 b = *reinterpret_cast<const v8*>(bias + n);
+    if (g.bias) {
+      const v8 b = *reinterpret_cast<const v8*>(bias);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] += (float)b[j];
     }
-    if (pre) {
+    if (g.pre) {
       v8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
-      *reinterpret_cast<v8*>(pre + m * g.ldp + n) = o;
+      *reinterpret_cast<v8*>(pre) = o;
     }
-    if (g.act) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = act_rt(z[j], g.act);
-    }
-    if (res) {
-      const v8 r = *reinterpret_cast<const v8*>(res + m * g.ldr + n);
+    act_rt<8>(z, g.act);
+    if (g.res) {
+      const v8 r = *reinterpret_cast<const v8*>(res);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] += (float)r[j];
     }
     if (g.out_f32) {
-      f8* out = reinterpret_cast<f8*>(static_cast<float*>(g.out) + m * g.ldo + n);
       f8 o;
       if (g.accumulate) {
-        o = *out;
+        o = *reinterpret_cast<f8*>(out32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] += o[j];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = z[j];
-      *out = o;
+      *reinterpret_cast<f8*>(out32) = o;
     } else {
-      v8* out = reinterpret_cast<v8*>(static_cast<T*>(g.out) + m * g.ldo + n);
       v8 o;
       if (g.accumulate) {
-        o = *out;
+        o = *reinterpret_cast<v8*>(out16);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] += (float)o[j];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
-      *out = o;
+      *reinterpret_cast<v8*>(out16) = o;
     }
     return;
   }
+  const uint32_t left = g.n - n;
 #pragma unroll
   for (int j = 0; j < 7; ++j) {
-    if (n + j >= g.n) break;
-    float v = z[j];
-    if (bias) v += (float)bias[n + j];
-    if (pre) pre[m * g.ldp + n + j] = (T)v;
-    v = act_rt(v, g.act);
-    if (res) v += (float)res[m * g.ldr + n + j];
+    if (j >= (int)left) break;
+    float v[1] = {z[j]};
+    if (g.bias) v[0] += (float)bias[j];
+    if (g.pre) pre[j] = (T)v[0];
+    if (g.act) act_rt<1>(v, g.act);
+    if (g.res) v[0] += (float)res[j];
     if (g.out_f32) {
-      float* out = static_cast<float*>(g.out) + m * g.ldo + n + j;
-      *out = g.accumulate ? v + *out : v;
+      out32[j] = g.accumulate ? v[0] + out32[j] : v[0];
     } else {
-      T* out = static_cast<T*>(g.out) + m * g.ldo + n + j;
-      *out = (T)(g.accumulate ? v + (float)*out : v);
+      out16[j] = (T)(g.accumulate ? v[0] + (float)out16[j] : v[0]);
     }
   }
 }

@@ -29,7 +29,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 constexpr int kStepK = kGemmStep;
 constexpr int kStages = 2;  // LDS stages
 
-__device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
+[[maybe_unused]] __device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
 #if ZERO_GEMM_DT == 2
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 #else
@@ -66,7 +66,10 @@ struct Tile {
   static_assert(kChunks % NT == 0, "whole rounds");
   static constexpr int kElems = R * kStepK;
 
-  static __device__ __forceinline__ int swz(int k) { return R % 128 == 0 ? (k & 3) << 1 : k & 2; }
+  static __device__ __forceinline__ int swz(int k) {
+    static_assert(R % 128 == 0 || R == 64 || R == 32, "whole granules, apart in 256 bytes");
+    return R % 128 == 0 ? (k & 3) << 1 : R == 64 ? k & 2 : 0;
+  }
 
   // (row, k) of the chunk that lies at place q of the tile
   static __device__ __forceinline__ void chunk_at(int q, int& row, int& k) {
@@ -103,6 +106,30 @@ struct Tile {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (__attribute__((address_space(3))) void*)(lds + (r * NT + wave * 64) * 8), 16,
           past ? 0xfffffff0u : voff[r], 0, 0, 0);
+  }
+
+  // By way of registers, for operands off the 16 bytes that the direct loads need: chunks at any
+  // element, and single elements at the edges.
+  t8 held[kRounds];
+  __device__ __forceinline__ void fetch(const T* base, uint64_t ld, uint32_t rows_left, int k_left, int tid) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      int row, k;
+      chunk_at(r * NT + tid, row, k);
+      const T* p = base + (KM ? (uint64_t)k * ld + row : (uint64_t)row * ld + k);
+      const int have = KM ? (k < k_left ? (int)rows_left - row : 0)
+                          : (row < (int)rows_left ? k_left - k : 0);
+      if (have >= 8) {
+        held[r] = *reinterpret_cast<const t8u*>(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) held[r][j] = j < have ? p[j] : (T)0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(T* lds, int tid) const {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) *reinterpret_cast<t8*>(lds + (r * NT + tid) * 8) = held[r];
   }
 
   // Fragment for 32 rows from row0 and 16 k from kk*16, read from LDS.
@@ -155,15 +182,17 @@ struct Frags {
 // fragments of the stage at da and db, which no wave reads any more: the loads of the step after
 // the next go there, while the products run through the stage at sa and sb. The stages are declared
 // apart, so that the reads of one need not wait for what is on its way into the other.
-template <typename S>
+template <typename S, bool DIRECT>
 __device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restrict__ sb,
                                      T* __restrict__ da, T* __restrict__ db, const typename S::A& ta,
                                      const typename S::B& tb, const T* pa, uint32_t abytes, const T* pb,
                                      uint32_t bbytes, int k_left, Frags<S>& f, f16v (&acc)[S::TM][S::TN],
                                      int wm0, int wn0, int wave, int lane) {
   Frags<S> h;
-  ta.dma(pa, abytes, k_left, da, wave);
-  tb.dma(pb, bbytes, k_left, db, wave);
+  if (DIRECT) {
+    ta.dma(pa, abytes, k_left, da, wave);
+    tb.dma(pb, bbytes, k_left, db, wave);
+  }
   h.load(sa, sb, 0, wm0, wn0, lane);
   f.mul(acc);
   f.load(sa, sb, 1, wm0, wn0, lane);
@@ -190,8 +219,9 @@ __device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restri
   }
 }
 
-template <typename S, int BM, int BN, int WM, int WN>
+template <typename S, bool DIRECT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass has no use for the body
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* lds = reinterpret_cast<T*>(smem);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -205,8 +235,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
 
   typename S::A ta;
   typename S::B tb;
-  ta.init(g.lda, tid);
-  tb.init(g.ldb, tid);
+  if (DIRECT) {
+    ta.init(g.lda, tid);
+    tb.init(g.ldb, tid);
+  }
   Cursor<T, kAK, BM> ca(g.a, g.lda, m0, g.m, k_begin);
   Cursor<T, kBK, BN> cb(g.b, g.ldb, n0, g.n, k_begin);
 
@@ -214,12 +246,19 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
   int k_left = (int)(g.k - k_begin);
   // k's last, partial chunk of a k-contiguous row comes with what lies behind the row
-  const int part = k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
+  const int part = DIRECT && k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
   const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
   Frags<S> f = {};
   if (steps > 0) {
-    ta.dma(ca.p, ca.bytes(k_left), k_left, lds, wave);
-    tb.dma(cb.p, cb.bytes(k_left), k_left, lds + S::kB, wave);
+    if (DIRECT) {
+      ta.dma(ca.p, ca.bytes(k_left), k_left, lds, wave);
+      tb.dma(cb.p, cb.bytes(k_left), k_left, lds + S::kB, wave);
+    } else {
+      ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
+      tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
+      ta.put(lds, tid);
+      tb.put(lds + S::kB, tid);
+    }
   }
   auto body = [&](auto parity, bool last) {
     constexpr int P = decltype(parity)::value;
@@ -237,8 +276,17 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
       zero_partial<T, kBK, BN>(sb, k_last, tid, S::NT);
       __syncthreads();
     }
-    step<S>(sa, sb, lds + (1 - P) * S::A::kElems, lds + S::kB + (1 - P) * S::B::kElems, ta, tb, ca.p,
-            abytes, cb.p, bbytes, k_left, f, acc, wm0, wn0, wave, lane);
+    T *da = lds + (1 - P) * S::A::kElems, *db = lds + S::kB + (1 - P) * S::B::kElems;
+    if (!DIRECT) {
+      ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
+      tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
+    }
+    step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, k_left, f, acc, wm0, wn0, wave,
+                    lane);
+    if (!DIRECT) {
+      ta.put(da, tid);
+      tb.put(db, tid);
+    }
   };
   for (int s = 0; s < steps; s += 2) {
     body(Int<0>{}, s + 1 == steps);
@@ -248,38 +296,47 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // the last step's loads past the end land before LDS is reused
   __syncthreads();
   // 32 rows at a time through LDS: the matrix instruction leaves a lane 4 neighbouring columns of
-  // one row; the epilogue wants 8 lanes on a row's 64 columns
-  float* stage = reinterpret_cast<float*>(smem) + wave * (32 * (S::TN * 32 + 4));
-  constexpr int LDSR = S::TN * 32 + 4;
-#pragma unroll
+  // one row; the epilogue wants 8 columns a lane, and a row's lanes side by side. One copy of its
+  // code for all (it would be the larger part of the kernel, fetched cold by every launch).
+  constexpr int kRow = S::TN * 32 + 4;
+  constexpr int kLanes = S::TN * 32 / 8;  // lanes on a row
+  float* stage = reinterpret_cast<float*>(smem) + wave * (32 * kRow);
+#pragma unroll 1
   for (int i = 0; i < S::TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < S::TN; ++j)
+    for (int c = 0; c < S::TM; ++c)
+      if (c == i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float4 v = make_float4(acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]);
-        *reinterpret_cast<float4*>(stage + (lane & 31) * LDSR + j * 32 + q * 8 + (lane >> 5) * 4) = v;
+        for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(stage + (lane & 31) * kRow + j * 32 + q * 8 + (lane >> 5) * 4) =
+                make_float4(acc[c][j][q * 4], acc[c][j][q * 4 + 1], acc[c][j][q * 4 + 2],
+                            acc[c][j][q * 4 + 3]);
       }
     __builtin_amdgcn_wave_barrier();
-    constexpr int LPR = S::TN * 32 / 8;    // lanes on a row
-    constexpr int RPP = 64 / LPR;          // rows of a pass
-    for (int r = lane / LPR; r < 32; r += RPP) {
-      const uint32_t m = m0 + wm0 + i * 32 + r, n = n0 + wn0 + (lane % LPR) * 8;
+#pragma unroll 1
+    for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
+      const uint32_t m = m0 + wm0 + i * 32 + r, n = n0 + wn0 + (lane % kLanes) * 8;
+      const float* at = stage + r * kRow + (lane % kLanes) * 8;
       float z[8];
-      *reinterpret_cast<float4*>(z) = *reinterpret_cast<float4*>(stage + r * LDSR + (lane % LPR) * 8);
-      *reinterpret_cast<float4*>(z + 4) = *reinterpret_cast<float4*>(stage + r * LDSR + (lane % LPR) * 8 + 4);
+      *reinterpret_cast<float4*>(z) = *reinterpret_cast<const float4*>(at);
+      *reinterpret_cast<float4*>(z + 4) = *reinterpret_cast<const float4*>(at + 4);
       if (m < g.m && n < g.n) finish<T>(g, z, m, n);
     }
     __builtin_amdgcn_wave_barrier();
   }
+#endif
 }
 
-template <int BM, int BN, int WM, int WN>
+// The 256 x 256 tile takes direct loads only: with the operands held in registers on their way it
+// would spill.
+template <bool DIRECT, int BM, int BN, int WM, int WN>
 hipError_t launch(const GemmDev& g, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
   constexpr int epi = WM * WN * 32 * (S::TN * 32 + 4) * 4;
   constexpr int lds = S::kElems * 2 > epi ? S::kElems * 2 : epi;
-  auto fn = k_gemm<S, BM, BN, WM, WN>;
+  auto fn = k_gemm<S, DIRECT, BM, BN, WM, WN>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -294,12 +351,14 @@ hipError_t launch(const GemmDev& g, hipStream_t s) {
 #define ZERO_CAT_(a, b, c, d) a##b##c##d
 #define ZERO_CAT(a, b, c, d) ZERO_CAT_(a, b, c, d)
 hipError_t ZERO_CAT(gemm_tiles_, ZERO_GEMM_DT, ZERO_GEMM_AK, ZERO_GEMM_BK)(const GemmDev& g, int shape,
-                                                                           hipStream_t s) {
+                                                                           bool direct, hipStream_t s) {
+#define ZERO_SHAPE(id, ...) \
+  case id: return direct ? launch<true, __VA_ARGS__>(g, s) : launch<id == 0, __VA_ARGS__>(g, s);
   switch (shape) {
-    case 0: return launch<256, 256, 2, 4>(g, s);
-    case 1: return launch<128, 128, 2, 2>(g, s);
+    ZERO_GEMM_SHAPES
     default: return hipErrorInvalidValue;
   }
+#undef ZERO_SHAPE
 }
 
 }  // namespace zero
