@@ -541,67 +541,84 @@ _ACTS = {"none": ZERO_ACT_NONE, "relu": ZERO_ACT_RELU, "gelu": ZERO_ACT_GELU,
          "gelu_tanh": ZERO_ACT_GELU_TANH, "silu": ZERO_ACT_SILU}
 
 
-def _here(t, what: str):
-    """The library launches on the current device: a tensor elsewhere is refused."""
+# These calls are short enough that their marshalling shows (a one-row layer takes the GPU about as
+# long), so every tensor is looked at once, by plain attribute reads.
+
+def _here() -> int:
+    """The device the library launches on: tensors elsewhere are refused."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, here: int) -> int | None:
+    if stream is None and _raw_stream is not None and here >= 0:
+        return _raw_stream(here)
+    return _stream(stream)
+
+
+def _refuse(t, what: str, dtype, here: int):
+    """The error for a tensor that _mat or _vec cannot take, whatever is wrong with it."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, {dtype} expected")
+    if t.get_device() != here:
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{here}")
+    raise TypeError(f"{what} cannot be used")
 
 
-def _mat(t, rows: int, cols: int, what: str, dtype) -> tuple[int | None, int]:
+def _mat(t, rows: int, cols: int, what: str, dtype, here: int):
     """(address, leading dimension) of a row-major (rows, cols) device matrix, or (None, cols)."""
     if t is None:
         return None, cols
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a device tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, {dtype} expected")
-    if tuple(t.shape) != (rows, cols):
+    if isinstance(t, torch.Tensor) and t.shape != (rows, cols):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, ({rows}, {cols}) expected")
-    if cols > 1 and t.numel() and t.stride(1) != 1:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != here or here < 0:
+        _refuse(t, what, dtype, here)
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1 and rows:
         raise ValueError(f"{what}: the elements of a row must be adjacent")
-    _here(t, what)
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    return t.data_ptr(), (ld if rows > 1 else cols)
 
 
-def _vec(t, n: int, what: str, dtype) -> int | None:
+def _vec(t, n: int, what: str, dtype, here: int):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a device tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, {dtype} expected")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != here or here < 0:
+        _refuse(t, what, dtype, here)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous elements expected")
-    _here(t, what)
     return t.data_ptr()
 
 
-def _param(t, rows: int, cols: int, what: str, dtype) -> int | None:
+def _param(t, rows: int, cols: int, what: str, dtype, here: int):
     """A parameter or its gradient: (rows, cols), contiguous, as it lies in the flat space."""
-    ptr, ld = _mat(t, rows, cols, what, dtype)
-    if t is not None and rows > 1 and cols and ld != cols:
+    ptr, ld = _mat(t, rows, cols, what, dtype, here)
+    if ld != cols and rows > 1 and cols:
         raise ValueError(f"{what} must be contiguous")
     return ptr
 
 
-def _workspace(t) -> tuple[int | None, int]:
+def _workspace(t, here: int):
     if t is None:
         return None, 0
     if not isinstance(t, torch.Tensor) or not t.is_contiguous():
         raise TypeError("workspace must be a contiguous device tensor")
-    _here(t, "workspace")
+    if t.get_device() != here or here < 0:
+        _refuse(t, "workspace", t.dtype, here)
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _linear_shape(x, weight, rows: int, act) -> ZeroLinearShape:
+def _linear_shape(weight, rows: int, act) -> ZeroLinearShape:
     kind = _ACTS.get(act, act)
     if not isinstance(kind, int):
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(_ACTS)}")
-    if weight.dtype not in (torch.bfloat16, torch.float16):
+    if weight.dtype is not torch.bfloat16 and weight.dtype is not torch.float16:
         raise TypeError("the linear layer takes bfloat16 or float16")
-    return ZeroLinearShape(rows, weight.shape[1], weight.shape[0], _TORCH_DT[weight.dtype], kind)
+    n, k = weight.shape
+    return ZeroLinearShape(rows, k, n, _TORCH_DT[weight.dtype], kind)
 
 
 def zero_linear_workspace_bytes(rows: int, in_features: int, out_features: int,
@@ -617,15 +634,16 @@ def zero_linear_forward(x, weight, out, bias=None, residual=None, act="none", pr
     gathered layer; ``workspace``: a device tensor of zero_linear_workspace_bytes."""
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor) or x.dim() != 2 or weight.dim() != 2:
         raise TypeError("x and weight must be 2-D device tensors")
-    dt = weight.dtype
-    s = _linear_shape(x, weight, x.shape[0], act)
-    M, K, N = s.rows, s.in_features, s.out_features
     if out is None:
         raise TypeError("out must be a device tensor")
+    dt, here, M = weight.dtype, _here(), x.shape[0]
+    s = _linear_shape(weight, M, act)
+    K, N = s.in_features, s.out_features
     _check(lib().zero_linear_forward(
-        ctypes.byref(s), *_mat(x, M, K, "x", dt), _param(weight, N, K, "weight", dt),
-        _vec(bias, N, "bias", dt), *_mat(residual, M, N, "residual", dt), *_mat(pre, M, N, "pre", dt),
-        *_mat(out, M, N, "out", dt), *_workspace(workspace), _stream(stream)), "zero_linear_forward")
+        ctypes.byref(s), *_mat(x, M, K, "x", dt, here), _param(weight, N, K, "weight", dt, here),
+        _vec(bias, N, "bias", dt, here), *_mat(residual, M, N, "residual", dt, here),
+        *_mat(pre, M, N, "pre", dt, here), *_mat(out, M, N, "out", dt, here), *_workspace(workspace, here),
+        _stream_on(stream, here)), "zero_linear_forward")
 
 
 def zero_linear_backward(dy, x, weight, act="none", pre=None, dz=None, dx=None, dweight=None,
@@ -637,22 +655,22 @@ def zero_linear_backward(dy, x, weight, act="none", pre=None, dz=None, dx=None, 
     for t in (dy, x, weight):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise TypeError("dy, x and weight must be 2-D device tensors")
-    dt = weight.dtype
-    s = _linear_shape(x, weight, dy.shape[0], act)
-    M, K, N = s.rows, s.in_features, s.out_features
-    grads = [t for t in (dweight, dbias) if t is not None]
-    gdt = grads[0].dtype if grads else dt
+    dt, here, M = weight.dtype, _here(), dy.shape[0]
+    s = _linear_shape(weight, M, act)
+    K, N = s.in_features, s.out_features
+    g = dweight if dweight is not None else dbias
+    gdt = dt if g is None else g.dtype
     if gdt not in _TORCH_DT:
         raise TypeError("dweight and dbias: the weight's dtype or float32")
     _check(lib().zero_linear_backward(
-        ctypes.byref(s), *_mat(dy, M, N, "dy", dt), *_mat(x, M, K, "x", dt),
-        _param(weight, N, K, "weight", dt), *_mat(pre, M, N, "pre", dt), *_mat(dz, M, N, "dz", dt),
-        *_mat(dx, M, K, "dx", dt), _param(dweight, N, K, "dweight", gdt), _vec(dbias, N, "dbias", gdt),
-        _TORCH_DT[gdt], int(bool(accumulate)), *_workspace(workspace), _stream(stream)),
-        "zero_linear_backward")
+        ctypes.byref(s), *_mat(dy, M, N, "dy", dt, here), *_mat(x, M, K, "x", dt, here),
+        _param(weight, N, K, "weight", dt, here), *_mat(pre, M, N, "pre", dt, here),
+        *_mat(dz, M, N, "dz", dt, here), *_mat(dx, M, K, "dx", dt, here),
+        _param(dweight, N, K, "dweight", gdt, here), _vec(dbias, N, "dbias", gdt, here), _TORCH_DT[gdt],
+        int(bool(accumulate)), *_workspace(workspace, here), _stream_on(stream, here)), "zero_linear_backward")
 
 
-def _distill_in(logits, top_index, top_logits, temperature, tail, weight) -> ZeroDistillIn:
+def _distill_in(logits, top_index, top_logits, temperature, tail, weight, here: int) -> ZeroDistillIn:
     for t, what in ((logits, "logits"), (top_index, "top_index"), (top_logits, "top_logits")):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise TypeError(f"{what} must be a 2-D device tensor")
@@ -662,17 +680,17 @@ def _distill_in(logits, top_index, top_logits, temperature, tail, weight) -> Zer
         raise TypeError("top_index must be int32 or int64")
     R, V = logits.shape
     K = top_index.shape[1]
-    if tuple(top_index.shape) != (R, K) or tuple(top_logits.shape) != (R, K):
+    if top_index.shape != (R, K) or top_logits.shape != (R, K):
         raise ValueError("top_index and top_logits must be (rows, topk) alike")
-    lp, ldl = _mat(logits, R, V, "logits", logits.dtype)
-    ip, ldi = _mat(top_index, R, K, "top_index", top_index.dtype)
-    tp, ldt = _mat(top_logits, R, K, "top_logits", top_logits.dtype)
+    lp, ldl = _mat(logits, R, V, "logits", logits.dtype, here)
+    ip, ldi = _mat(top_index, R, K, "top_index", top_index.dtype, here)
+    tp, ldt = _mat(top_logits, R, K, "top_logits", top_logits.dtype, here)
     if ldi != ldt:
         raise ValueError("top_index and top_logits must have the same row stride")
     f32 = torch.float32
     return ZeroDistillIn(R, V, K, _TORCH_DT[logits.dtype], _TORCH_DT[top_logits.dtype],
                          top_index.element_size(), float(temperature), lp, ldl, ip, tp, ldt,
-                         _vec(tail, R, "tail", f32), _vec(weight, R, "weight", f32))
+                         _vec(tail, R, "tail", f32, here), _vec(weight, R, "weight", f32, here))
 
 
 def zero_distill_forward(logits, top_index, top_logits, temperature: float, loss, stats, tail=None,
@@ -680,10 +698,10 @@ def zero_distill_forward(logits, top_index, top_logits, temperature: float, loss
     """loss[r] = weight[r] * KL(teacher || student) over the teacher's top entries of row r (an entry
     of index -1 is none; ``tail``: the log of the teacher's remaining mass, float32). ``loss``:
     float32 (rows,); ``stats``: float32 (rows, 2), kept for zero_distill_backward."""
-    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
-    f32 = torch.float32
-    _check(lib().zero_distill_forward(ctypes.byref(a), _vec(loss, a.rows, "loss", f32),
-                                      _vec(stats, 2 * a.rows, "stats", f32), _stream(stream)),
+    here, f32 = _here(), torch.float32
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight, here)
+    _check(lib().zero_distill_forward(ctypes.byref(a), _vec(loss, a.rows, "loss", f32, here),
+                                      _vec(stats, 2 * a.rows, "stats", f32, here), _stream_on(stream, here)),
            "zero_distill_forward")
 
 
@@ -691,23 +709,23 @@ def zero_distill_backward(logits, top_index, top_logits, temperature: float, sta
                           weight=None, upstream=None, scale: float = 1.0, stream=None):
     """dlogits = scale * upstream[r] * the gradient of loss[r] (``upstream``: float32 (rows,) or None);
     ``dlogits`` may be ``logits`` itself."""
-    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
-    f32 = torch.float32
+    here, f32 = _here(), torch.float32
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight, here)
     _check(lib().zero_distill_backward(
-        ctypes.byref(a), _vec(stats, 2 * a.rows, "stats", f32), _vec(upstream, a.rows, "upstream", f32),
-        float(scale), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype), _stream(stream)),
+        ctypes.byref(a), _vec(stats, 2 * a.rows, "stats", f32, here), _vec(upstream, a.rows, "upstream", f32, here),
+        float(scale), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype, here), _stream_on(stream, here)),
         "zero_distill_backward")
 
 
 def zero_distill_step(logits, top_index, top_logits, temperature: float, loss, dlogits, tail=None,
                       weight=None, upstream=None, scale: float = 1.0, stream=None):
     """zero_distill_forward and zero_distill_backward in one pass over the logits."""
-    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight)
-    f32 = torch.float32
+    here, f32 = _here(), torch.float32
+    a = _distill_in(logits, top_index, top_logits, temperature, tail, weight, here)
     _check(lib().zero_distill_step(
-        ctypes.byref(a), _vec(upstream, a.rows, "upstream", f32), float(scale),
-        _vec(loss, a.rows, "loss", f32), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype),
-        _stream(stream)), "zero_distill_step")
+        ctypes.byref(a), _vec(upstream, a.rows, "upstream", f32, here), float(scale),
+        _vec(loss, a.rows, "loss", f32, here), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype, here),
+        _stream_on(stream, here)), "zero_distill_step")
 
 
 # ------------------------------------------------------------------------------ host (offload) calls

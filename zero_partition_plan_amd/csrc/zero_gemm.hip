@@ -33,13 +33,118 @@ __global__ __launch_bounds__(256) void k_join(GemmDev g) {
   }
 }
 
+// A few rows (16 or 32) times a matrix of k-contiguous rows, where reading that matrix once is all there
+// is to do: 16 of its rows a block, straight from memory into the matrix instruction's registers,
+// the waves taking turns along k and joined through LDS in their order. No split over blocks, so
+// one launch. Any alignment; rows past the end repeat the last one and are not stored.
+template <typename T, int MT>
+__global__ __launch_bounds__(1024) void k_few(GemmDev g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef T v8 __attribute__((ext_vector_type(8)));
+  typedef T v8u __attribute__((ext_vector_type(8), aligned(2)));
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  constexpr int U = 8;                      // loads in flight per row and wave
+  __shared__ float red[16][MT * 16][20];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const uint32_t n0 = blockIdx.x * 16, r = lane & 15;
+  const uint32_t kq = (lane >> 4) * 8;
+  const uint32_t n = n0 + r < g.n ? n0 + r : g.n - 1;
+  const T* w = static_cast<const T*>(g.b) + (uint64_t)n * g.ldb;
+  const T* x[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const uint32_t m = t * 16 + r < g.m ? t * 16 + r : g.m - 1;
+    x[t] = static_cast<const T*>(g.a) + (uint64_t)m * g.lda;
+  }
+  f4 acc[MT] = {};
+  auto mul = [&](v8 a, const v8* b) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if constexpr (sizeof(T) == 2 && __is_same(T, __bf16))
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[t], acc[t], 0, 0, 0);
+      else
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[t], 0, 0, 0);
+    }
+  };
+  for (uint64_t k0 = (uint64_t)wave * (32 * U); k0 < g.k; k0 += (uint64_t)waves * (32 * U)) {
+    if (k0 + 32 * U <= g.k) {
+      v8 a[U], b[U][MT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) a[u] = *reinterpret_cast<const v8u*>(w + k0 + u * 32 + kq);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) b[u][t] = *reinterpret_cast<const v8u*>(x[t] + k0 + u * 32 + kq);
+#pragma unroll
+      for (int u = 0; u < U; ++u) mul(a[u], b[u]);
+    } else {
+      for (uint64_t k1 = k0; k1 < g.k; k1 += 32) {
+        const int have = (int)(g.k - k1) - (int)kq;
+        v8 a, b[MT];
+        if (have >= 8) {
+          a = *reinterpret_cast<const v8u*>(w + k1 + kq);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) b[t] = *reinterpret_cast<const v8u*>(x[t] + k1 + kq);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            a[j] = j < have ? w[k1 + kq + j] : (T)0.0f;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) b[t][j] = j < have ? x[t][k1 + kq + j] : (T)0.0f;
+          }
+        }
+        mul(a, b);
+      }
+    }
+  }
+  // a lane holds 4 neighbouring columns n of row m
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+    *reinterpret_cast<f4*>(&red[wave][t * 16 + r][(lane >> 4) * 4]) = acc[t];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * 256; i += blockDim.x) {
+    float v = red[0][i >> 4][i & 15];
+    for (int s = 1; s < waves; ++s) v += red[s][i >> 4][i & 15];
+    red[0][i >> 4][i & 15] = v;
+  }
+  __syncthreads();
+  const uint32_t m = threadIdx.x >> 1, nn = n0 + (threadIdx.x & 1) * 8;
+  if (m < MT * 16 && m < g.m && nn < g.n) {
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = red[0][m][(threadIdx.x & 1) * 8 + j];
+    finish_row<T>(g, z, m, nn);
+  }
+#endif
+}
+
+constexpr uint32_t kFewRows = 32;
+bool few(const GemmArgs& g) { return g.m <= kFewRows && !g.a_kmajor && !g.b_kmajor; }
+
+template <typename T>
+hipError_t run_few(const GemmDev& d, hipStream_t s) {
+  const uint32_t blocks = (d.n + 15) / 16;
+  uint32_t waves = 2048 / blocks;
+  const uint32_t most = (d.k + 255) / 256;
+  waves = waves > most ? most : waves;
+  waves = waves < 4 ? 4 : waves > 16 ? 16 : waves;
+  if (d.m <= 16) k_few<T, 1><<<dim3(blocks), dim3(waves * 64), 0, s>>>(d);
+  else k_few<T, 2><<<dim3(blocks), dim3(waves * 64), 0, s>>>(d);
+  return hipGetLastError();
+}
+
+// What a tile of each shape takes, in us on MI355X: `fixed` besides its steps (start, epilogue), a
+// step (64 k) with the card almost empty and with `per_cu` tiles on every CU. Fitted to products
+// of 333 to 8192 rows; tiles of 128 x 128 and less win where there are few, as their fixed part
+// is shorter, tiles of 256 x 256 where there are many, as they read least.
 struct TileShape {
   uint32_t bm, bn, per_cu;
-  float cost;  // time of one step of one tile, relative
+  float fixed, alone, full;
 };
-constexpr TileShape kShapes[] = {{256, 256, 1, 1.0f},  {128, 256, 1, 0.58f}, {256, 128, 1, 0.58f},
-                                 {128, 128, 2, 0.30f}, {64, 256, 2, 0.32f},  {32, 256, 2, 0.22f},
-                                 {64, 64, 5, 0.10f}};
+constexpr TileShape kShapes[] = {{256, 256, 1, 7.0f, 1.0f, 1.45f},  {128, 256, 1, 6.5f, 0.58f, 0.92f},
+                                 {256, 128, 1, 6.5f, 0.62f, 0.94f}, {128, 128, 2, 5.4f, 0.43f, 0.87f},
+                                 {64, 256, 2, 5.5f, 0.43f, 0.95f},  {32, 256, 2, 4.2f, 0.41f, 0.81f},
+                                 {64, 64, 5, 3.4f, 0.27f, 1.0f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 constexpr uint32_t kCus = 256;
 
@@ -48,24 +153,27 @@ struct Plan {
   uint32_t splits, k_split;
 };
 
+// The shape and the split of k with the least predicted time. By sizes alone: the workspace must
+// not depend on alignment.
 Plan plan(uint64_t m, uint64_t n, uint64_t k) {
-  Plan best{0, 1, 0};
-  float best_t = 1e30f;
   const uint64_t steps = k ? (k + kGemmStep - 1) / kGemmStep : 1;
-  best.k_split = (uint32_t)(steps * kGemmStep);
+  Plan best{0, 1, (uint32_t)(steps * kGemmStep)};
+  float best_t = 1e30f;
   for (int i = 0; i < kNumShapes; ++i) {
     const TileShape& t = kShapes[i];
     const uint64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
-    for (uint64_t sp = 1; sp <= 16 && (sp == 1 || steps / sp >= 4); ++sp) {
-      const uint64_t per = (steps + sp - 1) / sp;
-      const uint64_t slots = kCus * t.per_cu;
-      const uint64_t rounds = (tiles * sp + slots - 1) / slots;
-      // k_join and the workspace's write and read, in units of a 256 x 256 x 64 step (about 1.2 us)
-      const float join = sp > 1 ? 3.0f + (float)(m * n * sp * 8) / 8e6f : 0.0f;
-      const float time = (float)(rounds * (per + 4)) * t.cost * t.per_cu + join;
+    const uint64_t slots = kCus * t.per_cu;
+    for (uint64_t sp = 1; sp <= 32 && (sp == 1 || steps / sp >= 2); ++sp) {
+      const uint64_t per = (steps + sp - 1) / sp, splits = (steps + per - 1) / per;
+      const uint64_t all = tiles * splits, rounds = all / slots, rest = all % slots;
+      float time = (float)rounds * (t.fixed + (float)per * t.full);
+      if (rest)
+        time += t.fixed + (float)per * (t.alone + (t.full - t.alone) * (float)rest / (float)slots);
+      // the join's launch, and the partial sums written and read at some 4 TB/s
+      if (splits > 1) time += 2.5f + (float)(m * n * splits) * 8.0f / 4e6f;
       if (time < best_t) {
         best_t = time;
-        best = Plan{i, (uint32_t)((steps + per - 1) / per), (uint32_t)(per * kGemmStep)};
+        best = Plan{i, (uint32_t)splits, (uint32_t)(per * kGemmStep)};
       }
     }
   }
@@ -80,8 +188,8 @@ bool direct(const void* p, uint64_t ld) {
 
 }  // namespace
 
-uint64_t gemm_workspace_bytes(uint64_t m, uint64_t n, uint64_t k) {
-  if (!m || !n) return 0;
+uint64_t gemm_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, bool kmajor) {
+  if (!m || !n || (m <= kFewRows && !kmajor)) return 0;
   const Plan p = plan(m, n, k);
   return p.splits > 1 ? p.splits * m * n * 4 : 0;
 }
@@ -92,6 +200,7 @@ ZERO_TILES(2, 0, 0) ZERO_TILES(2, 0, 1) ZERO_TILES(2, 1, 1)
 
 hipError_t gemm(const GemmArgs& g, hipStream_t s) {
   const bool dir = direct(g.a, g.lda) && direct(g.b, g.ldb);
+  const bool bf = g.dtype == ZERO_BF16;
   Plan p = plan(g.m, g.n, g.k);
   if (!dir && p.shape == 0) p.shape = 1;  // the same splits, so the same workspace
   GemmDev d{};
@@ -102,8 +211,11 @@ hipError_t gemm(const GemmArgs& g, hipStream_t s) {
   d.tiles_n = (g.n + kShapes[p.shape].bn - 1) / kShapes[p.shape].bn;
   d.splits = p.splits, d.k_split = p.k_split;
   d.act = g.act, d.accumulate = g.accumulate, d.out_f32 = g.out_dtype == ZERO_F32;
+  if (few(g)) {
+    d.splits = 1;
+    return bf ? run_few<__bf16>(d, s) : run_few<_Float16>(d, s);
+  }
   if ((uint64_t)d.tiles_m * d.tiles_n > 0x7fffffffu) return hipErrorInvalidConfiguration;
-  const bool bf = g.dtype == ZERO_BF16;
   hipError_t e;
   if (!g.a_kmajor && !g.b_kmajor) e = bf ? gemm_tiles_200(d, p.shape, dir, s) : gemm_tiles_100(d, p.shape, dir, s);
   else if (!g.a_kmajor) e = bf ? gemm_tiles_201(d, p.shape, dir, s) : gemm_tiles_101(d, p.shape, dir, s);

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "zero_gemm.h"
 
 #ifndef ZERO_GEMM_DT
@@ -338,9 +340,16 @@ hipError_t launch(const GemmDev& g, hipStream_t s) {
   constexpr int lds = S::kElems * 2 > epi ? S::kElems * 2 : epi;
   auto fn = k_gemm<S, DIRECT, BM, BN, WM, WN>;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static std::atomic<uint64_t> allowed{0};  // one bit a device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+      allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   fn<<<dim3(g.tiles_m * g.tiles_n, g.splits), dim3(S::NT), lds, s>>>(g);
   return hipGetLastError();

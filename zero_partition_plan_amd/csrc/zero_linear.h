@@ -25,10 +25,10 @@ struct GemmArgs {
   void* pre;           // [m, n] or NULL
   void* out;           // [m, n]
   uint64_t ldr, ldp, ldo;
-  float* ws;           // gemm_workspace_bytes(m, n, k)
+  float* ws;           // gemm_workspace_bytes(m, n, k, a_kmajor || b_kmajor)
 };
 
 hipError_t gemm(const GemmArgs& g, hipStream_t stream);
-uint64_t gemm_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
+uint64_t gemm_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, bool kmajor);
 
 }  // namespace zero

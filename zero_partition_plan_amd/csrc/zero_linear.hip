@@ -13,36 +13,102 @@ namespace {
 
 constexpr uint64_t kMaxSize = 0x7fffffffu;
 
-// dz = round16(dy * act'(pre)), element by element.
+// dz = round16(dy * act'(pre)), 8 columns a thread, and the bias gradient's partial sums of the
+// stored dz: a block takes 256 columns and `chunk` rows, its 8 threads on a column every eighth row,
+// joined through LDS in a fixed order. One pass over dy and pre: memory is the bound. Without an
+// activation only the sums are formed.
+constexpr int kColsPerBlock = 256, kRowLanes = 8;
+
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void k_dz(const T* dy, uint64_t lddy, const T* pre, uint64_t ldp,
-                                            T* dz, uint64_t lddz, uint64_t rows, uint64_t cols) {
-  for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (uint64_t c = blockIdx.x * 256ull + threadIdx.x; c < cols; c += gridDim.x * 256ull)
-      dz[r * lddz + c] = (T)((float)dy[r * lddy + c] * act_slope<ACT>((float)pre[r * ldp + c]));
+                                            T* dz, uint64_t lddz, uint32_t rows, uint32_t cols,
+                                            uint32_t chunk, float* sums) {
+  typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
+  __shared__ float part[kRowLanes][kColsPerBlock + 4];
+  const int cl = threadIdx.x % 32, rl = threadIdx.x / 32;
+  const uint32_t c = blockIdx.x * kColsPerBlock + cl * 8;
+  const uint64_t first = (uint64_t)blockIdx.y * chunk;
+  const uint64_t end = first + chunk < rows ? first + chunk : rows;
+  float s[8] = {};
+  if (c + 8 <= cols) {
+#pragma unroll 2
+    for (uint64_t r = first + rl; r < end; r += kRowLanes) {
+      v8 d = *reinterpret_cast<const v8*>(dy + r * lddy + c);
+      if constexpr (ACT != ZERO_ACT_NONE) {
+        const v8 z = *reinterpret_cast<const v8*>(pre + r * ldp + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = (T)((float)d[j] * act_slope<ACT>((float)z[j]));
+        *reinterpret_cast<v8*>(dz + r * lddz + c) = d;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += (float)d[j];
+    }
+  } else {
+    for (uint64_t r = first + rl; r < end; r += kRowLanes)
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (c + j < cols) {
+          T d = dy[r * lddy + c + j];
+          if constexpr (ACT != ZERO_ACT_NONE) {
+            d = (T)((float)d * act_slope<ACT>((float)pre[r * ldp + c + j]));
+            dz[r * lddz + c + j] = d;
+          }
+          s[j] += (float)d;
+        }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[rl][cl * 8 + j] = s[j];
+  __syncthreads();
+  const uint32_t col = blockIdx.x * kColsPerBlock + threadIdx.x;
+  if (col >= cols) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int l = 0; l < kRowLanes; ++l) v += part[l][threadIdx.x];
+  sums[(uint64_t)blockIdx.y * cols + col] = v;
 }
 
-// dbias: one thread per column, rows in ascending order.
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void k_db(const T* dz, uint64_t ld, uint64_t rows, uint64_t cols,
-                                            O* db, int accumulate) {
-  const uint64_t c = blockIdx.x * 256ull + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.0f;
-  for (uint64_t r = 0; r < rows; ++r) s += (float)dz[r * ld + c];
-  if (accumulate) s += (float)db[c];
-  db[c] = (O)s;
+// dbias from the chunks' sums: 4 threads on a column, every fourth chunk each.
+template <typename O>
+__global__ __launch_bounds__(256) void k_db(const float* sums, uint32_t chunks, uint32_t cols, O* db,
+                                            int accumulate) {
+  __shared__ float part[4][64];
+  const int cl = threadIdx.x % 64, l = threadIdx.x / 64;
+  const uint32_t c = blockIdx.x * 64 + cl;
+  float v = 0.0f;
+  if (c < cols)
+#pragma unroll 4
+    for (uint32_t i = l; i < chunks; i += 4) v += sums[(uint64_t)i * cols + c];
+  part[l][cl] = v;
+  __syncthreads();
+  if (l || c >= cols) return;
+  v = (part[0][cl] + part[1][cl]) + (part[2][cl] + part[3][cl]);
+  if (accumulate) v += (float)db[c];
+  db[c] = (O)v;
+}
+
+// Row chunks of the pass: enough blocks to fill the card several times, 32 rows a chunk at least,
+// and at most 128, which the join still reads in a few microseconds.
+uint32_t dz_chunks(uint64_t rows, uint64_t cols) {
+  const uint64_t groups = (cols + kColsPerBlock - 1) / kColsPerBlock;
+  uint64_t n = (rows + 31) / 32;
+  const uint64_t most = groups < 16 ? 128 : 2048 / groups;
+  if (n > most) n = most ? most : 1;
+  return n ? (uint32_t)n : 1u;
 }
 
 template <typename T>
 hipError_t run_dz(int act, const void* dy, uint64_t lddy, const void* pre, uint64_t ldp, void* dz,
-                  uint64_t lddz, uint64_t rows, uint64_t cols, hipStream_t s) {
-  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(rows < 4096 ? rows : 4096));
+                  uint64_t lddz, uint64_t rows, uint64_t cols, float* sums, hipStream_t s) {
+  const uint32_t chunks = dz_chunks(rows, cols);
+  const uint32_t chunk = (uint32_t)((rows + chunks - 1) / chunks);
+  const dim3 grid((unsigned)((cols + kColsPerBlock - 1) / kColsPerBlock), chunks);
 #define ZERO_DZ(A)                                                                             \
   k_dz<T, A><<<grid, dim3(256), 0, s>>>(static_cast<const T*>(dy), lddy,                       \
                                         static_cast<const T*>(pre), ldp, static_cast<T*>(dz), \
-                                        lddz, rows, cols)
+                                        lddz, (uint32_t)rows, (uint32_t)cols, chunk, sums)
   switch (act) {
+    case ZERO_ACT_NONE: ZERO_DZ(ZERO_ACT_NONE); break;
     case ZERO_ACT_RELU: ZERO_DZ(ZERO_ACT_RELU); break;
     case ZERO_ACT_GELU: ZERO_DZ(ZERO_ACT_GELU); break;
     case ZERO_ACT_GELU_TANH: ZERO_DZ(ZERO_ACT_GELU_TANH); break;
@@ -52,11 +118,11 @@ hipError_t run_dz(int act, const void* dy, uint64_t lddy, const void* pre, uint6
   return hipGetLastError();
 }
 
-template <typename T, typename O>
-hipError_t run_db(const void* dz, uint64_t ld, uint64_t rows, uint64_t cols, void* db,
-                  int accumulate, hipStream_t s) {
-  k_db<T, O><<<dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, s>>>(
-      static_cast<const T*>(dz), ld, rows, cols, static_cast<O*>(db), accumulate);
+template <typename O>
+hipError_t run_db(const float* sums, uint64_t rows, uint64_t cols, void* db, int accumulate,
+                  hipStream_t s) {
+  k_db<O><<<dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, s>>>(
+      sums, dz_chunks(rows, cols), (uint32_t)cols, static_cast<O*>(db), accumulate);
   return hipGetLastError();
 }
 
@@ -153,10 +219,12 @@ extern "C" {
 uint64_t zero_linear_workspace_bytes(uint64_t rows, uint64_t in_features, uint64_t out_features,
                                      int32_t backward) {
   if (rows > kMaxSize || in_features > kMaxSize || out_features > kMaxSize) return 0;
-  if (!backward) return gemm_workspace_bytes(rows, out_features, in_features);
-  const uint64_t dx = gemm_workspace_bytes(rows, in_features, out_features);
-  const uint64_t dw = gemm_workspace_bytes(out_features, in_features, rows);
-  return dx > dw ? dx : dw;
+  if (!backward) return gemm_workspace_bytes(rows, out_features, in_features, false);
+  const uint64_t dx = gemm_workspace_bytes(rows, in_features, out_features, true);
+  const uint64_t dw = gemm_workspace_bytes(out_features, in_features, rows, true);
+  const uint64_t db = out_features * dz_chunks(rows, out_features) * 4;
+  const uint64_t most = dx > dw ? dx : dw;
+  return most > db ? most : db;
 }
 
 zero_status zero_linear_forward(const zero_linear_shape* s, const void* x, uint64_t ldx,
@@ -239,10 +307,19 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
   const bool bf = s->dtype == ZERO_BF16;
   const void* d = dy;
   uint64_t ldd = m[0].ld;
-  if (has_act && M && N) {
-    e = bf ? run_dz<__bf16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, strm)
-           : run_dz<_Float16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, strm);
-    d = dz, ldd = m[4].ld;
+  // the bias gradient's sums are joined before the products use the workspace for theirs
+  float* ws = static_cast<float*>(workspace);
+  const bool db_wanted = dbias && N && !(M == 0 && accumulate);
+  if ((has_act && M && N) || db_wanted) {
+    float* sums = db_wanted ? ws : nullptr;
+    e = bf ? run_dz<__bf16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, strm)
+           : run_dz<_Float16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, strm);
+  }
+  if (has_act) d = dz, ldd = m[4].ld;
+  if (e == hipSuccess && db_wanted) {
+    if (grad_dtype == ZERO_F32) e = run_db<float>(ws, M, N, dbias, accumulate, strm);
+    else if (bf) e = run_db<__bf16>(ws, M, N, dbias, accumulate, strm);
+    else e = run_db<_Float16>(ws, M, N, dbias, accumulate, strm);
   }
   if (e == hipSuccess && dx && M && K) {
     GemmArgs g{};
@@ -251,7 +328,7 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
     g.m = (uint32_t)M, g.n = (uint32_t)K, g.k = (uint32_t)N;
     g.dtype = g.out_dtype = s->dtype;
     g.out = dx, g.ldo = m[5].ld;
-    g.ws = static_cast<float*>(workspace);
+    g.ws = ws;
     e = gemm(g, strm);
   }
   if (e == hipSuccess && dweight && N && K && !(M == 0 && accumulate)) {
@@ -262,15 +339,8 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
     g.dtype = s->dtype, g.out_dtype = grad_dtype;
     g.accumulate = accumulate != 0;
     g.out = dweight, g.ldo = K;
-    g.ws = static_cast<float*>(workspace);
+    g.ws = ws;
     e = gemm(g, strm);
-  }
-  if (e == hipSuccess && dbias && N && !(M == 0 && accumulate)) {
-    const bool f32 = grad_dtype == ZERO_F32;
-    e = bf ? (f32 ? run_db<__bf16, float>(d, ldd, M, N, dbias, accumulate, strm)
-                  : run_db<__bf16, __bf16>(d, ldd, M, N, dbias, accumulate, strm))
-           : (f32 ? run_db<_Float16, float>(d, ldd, M, N, dbias, accumulate, strm)
-                  : run_db<_Float16, _Float16>(d, ldd, M, N, dbias, accumulate, strm));
   }
   return hip_result(fn, e);
 }
