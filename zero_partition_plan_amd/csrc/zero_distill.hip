@@ -1,12 +1,16 @@
 // Distillation from a teacher's top logits on gfx950: loss, gradient, and both.
 //
 // One block per row. In base-2 logarithms with c = log2(e)/T, m the row's largest logit and
-// s = sum over v of 2^((z_v - m) c):  log2 q_v = (z_v - m) c - log2 s. The row's logits are read
-// once with a running (m, s) per thread, joined in a fixed order. With a tail, the sum runs over
-// the entries that are not listed only (a bitmap in LDS says which), so that the student's
-// remaining mass comes from a sum of its own and not from 1 minus a sum close to 1; the listed
-// entries, at most 1024, are joined to it afterwards. The gradient is a second pass that writes
-// F * 2^((z_v - m) c) for every entry and then the listed ones over it.
+// s = sum over v of 2^((z_v - m) c):  log2 q_v = (z_v - m) c - log2 s. The first wave looks after the
+// teacher's entries while the others sum. With a tail, the sum runs over the entries that are not
+// listed only (a bitmap in LDS says which), so that the student's remaining mass comes from a
+// sum of its own and not from 1 minus a sum close to 1; the listed entries, at most 1024, are
+// joined to it afterwards. The gradient writes F * 2^((z_v - m) c) for every entry and then the
+// listed ones over it.
+//
+// Memory is the bound: the loss alone and the gradient alone read the row once, and the step keeps the
+// row in registers between the two, as far as it fits (a row of 131072 16-bit or 65536 fp32 logits);
+// longer rows are read twice, the second time mostly from cache.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -63,27 +67,6 @@ __device__ __forceinline__ MaxSum join(const Args& a, MaxSum x, MaxSum y) {
   return r;
 }
 
-__device__ __forceinline__ void block_join(const Args& a, MaxSum& v, MaxSum* lds) {
-  for (int o = 32; o; o >>= 1) v = join(a, v, MaxSum{__shfl_xor(v.m, o), __shfl_xor(v.s, o)});
-  const int wave = threadIdx.x / 64, waves = blockDim.x / 64;
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) lds[wave] = v;
-  __syncthreads();
-  v = lds[0];
-  for (int w = 1; w < waves; ++w) v = join(a, v, lds[w]);
-}
-
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  const int wave = threadIdx.x / 64, waves = blockDim.x / 64;
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) lds[wave] = v;
-  __syncthreads();
-  v = lds[0];
-  for (int w = 1; w < waves; ++w) v += lds[w];
-  return v;
-}
-
 __device__ __forceinline__ float load_as_float(const void* p, int32_t dtype, uint64_t i) {
   if (dtype == ZERO_F32) return static_cast<const float*>(p)[i];
   if (dtype == ZERO_F16) return (float)static_cast<const _Float16*>(p)[i];
@@ -98,12 +81,115 @@ struct Pack {
   typedef vec type;
 };
 
-template <typename T, bool TAIL, int MODE>
-__global__ __launch_bounds__(1024) void k_distill(Args a) {
-  extern __shared__ uint32_t lds[];
-  __shared__ MaxSum s_ms[16];
-  __shared__ float s_f[16];
-  __shared__ int s_dup;
+__device__ __forceinline__ float wave_sum(float v) {
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+__device__ __forceinline__ MaxSum wave_join(const Args& a, MaxSum v) {
+  for (int o = 32; o; o >>= 1) v = join(a, v, MaxSum{__shfl_xor(v.m, o), __shfl_xor(v.s, o)});
+  return v;
+}
+
+// What the first wave leaves for the others.
+struct Teacher {
+  MaxSum top;       // the listed entries' logits, each index once (tail only)
+  float log_sum;    // log2 of the teacher's sum, in the entries' own base-2 exponents s_y
+  float log_tail;   // log2 p_tail
+  float p_tail;
+  int dup;          // some index is listed twice
+  int none;         // no teacher mass
+};
+
+// The teacher's entries, by one wave: exponents s_y[k] (-inf: no mass), indices s_idx[k] (-1: no
+// entry) and the student's logits there.
+template <typename T, bool TAIL>
+__device__ __forceinline__ void teach(const Args& a, uint64_t row, const T* z, uint32_t* bits, int* s_idx,
+                                      float* s_y, float* s_z, Teacher* out) {
+  const zero_distill_in& in = a.in;
+  const uint32_t K = (uint32_t)in.topk;
+  const int lane = threadIdx.x;
+  float tmax = -INFINITY;
+  for (uint32_t k = lane; k < K; k += 64) {
+    const uint64_t e = row * in.ld_top + k;
+    const int64_t id = in.index_bytes == 8 ? static_cast<const int64_t*>(in.top_index)[e]
+                                           : static_cast<const int32_t*>(in.top_index)[e];
+    const bool valid = id >= 0 && id < (int64_t)in.vocab;
+    const float y = valid ? load_as_float(in.top_logits, in.teacher_dtype, e) : -INFINITY;
+    s_idx[k] = valid ? (int)id : -1;
+    s_y[k] = y;
+    s_z[k] = valid ? (float)z[id] : -INFINITY;
+    tmax = y > tmax || y != y ? y : tmax;
+  }
+  for (int o = 32; o; o >>= 1) {
+    const float x = __shfl_xor(tmax, o);
+    tmax = x > tmax || x != x ? x : tmax;
+  }
+  // the tail is given as a logarithm at temperature T; exponents are relative to the larger of the
+  // listed entries and the tail
+  const float ytail = TAIL ? in.tail[row] * 1.44269504088896340736f : -INFINITY;
+  const float over = mul_c(a, tmax) - ytail;  // +inf without a tail
+  const bool tail_first = over < 0.0f;
+  float sum = 0.0f;
+  int dup = 0;
+  for (uint32_t k = lane; k < K; k += 64) {
+    float y = s_y[k] == -INFINITY ? -INFINITY : mul_c(a, s_y[k] - tmax);
+    if (tail_first) y += over;
+    s_y[k] = y;
+    sum += exp2f(y);
+    if (s_idx[k] >= 0) {
+      const uint32_t bit = 1u << (s_idx[k] & 31);
+      if (atomicOr(&bits[s_idx[k] >> 5], bit) & bit) dup = 1;
+    }
+  }
+  dup = __any(dup);
+  const float y_rel = tail_first ? 0.0f : -over;
+  const float e_tail = TAIL ? exp2f(y_rel) : 0.0f;
+  sum = wave_sum(sum) + e_tail;
+  MaxSum top{kLowest, 0.0f};
+  if (TAIL) {
+    for (uint32_t k = lane; k < K; k += 64) {
+      bool leader = s_idx[k] >= 0;  // the first entry of its index
+      if (dup && leader)
+        for (uint32_t j = 0; j < k; ++j) leader &= s_idx[j] != s_idx[k];
+      if (leader)
+        top = join(a, top, MaxSum{s_z[k] > kLowest ? s_z[k] : kLowest, s_z[k] == -INFINITY ? 0.0f : 1.0f});
+      if (s_z[k] != s_z[k]) top.s = s_z[k];
+    }
+    top = wave_join(a, top);
+  }
+  if (lane == 0) {
+    out->top = top;
+    out->log_sum = log2f(sum);
+    out->log_tail = y_rel - log2f(sum);
+    out->p_tail = e_tail / sum;
+    out->dup = dup;
+    out->none = tmax == -INFINITY && ytail == -INFINITY;
+  }
+}
+
+// Adds n values to a running sum; those whose bit in `skip` is set are left out.
+template <typename T, int N>
+__device__ __forceinline__ void add(const Args& a, MaxSum& r, float (&f)[N], uint32_t skip) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] = skip >> j & 1 ? -INFINITY : f[j];
+  float m = f[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = f[j] > m ? f[j] : m;
+  if (m > r.m) {
+    r.s *= exp2f(mul_c(a, r.m - m));
+    r.m = m;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) r.s += __builtin_amdgcn_exp2f(mul_s<T>(a, f[j] - r.m));
+}
+
+// NV: 16-byte vectors of the row that a thread of the step holds in registers; 0: reads it again.
+template <typename T, bool TAIL, int MODE, int NV, int NT>
+__global__ __launch_bounds__(NT) void k_distill(Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+  __shared__ MaxSum s_ms[NT / 64];
+  __shared__ Teacher teacher;
   using V = typename Pack<T>::type;
   constexpr int W = Pack<T>::n;
   const zero_distill_in& in = a.in;
@@ -111,184 +197,183 @@ __global__ __launch_bounds__(1024) void k_distill(Args a) {
   const uint64_t row = blockIdx.x;
   const T* z = static_cast<const T*>(in.logits) + row * in.ld_logits;
   T* dz = static_cast<T*>(a.dlogits) + row * a.ldg;
-  const int t = threadIdx.x, nt = blockDim.x;
+  const int t = threadIdx.x, wave = t / 64;
+  const uint32_t body = vocab / W;               // whole vectors
+  const uint32_t last = body * W + t;            // a thread's element behind them, if < vocab
+  const uint32_t words = (vocab + 127) / 128 * 4;
+  uint32_t* bits = lds;
+  int* s_idx = reinterpret_cast<int*>(lds + words);
+  float* s_y = reinterpret_cast<float*>(lds + words + K);
+  float* s_z = reinterpret_cast<float*>(lds + words + 2 * K);
 
+  V held[NV ? NV : 1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (i * NT + t < (int)body) held[i] = *reinterpret_cast<const V*>(z + (uint64_t)(i * NT + t) * W);
+  for (uint32_t i = t; i < words / 4; i += NT)
+    reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
   const float w = in.weight ? in.weight[row] : 1.0f;
-  uint32_t* bits = lds;                                              // [ceil(vocab/32)]
-  const uint32_t words = (vocab + 31) / 32;
-  int* s_idx = reinterpret_cast<int*>(lds + words);                  // [K] -1: no entry
-  float* s_p = reinterpret_cast<float*>(lds + words + K);            // [K]
-  float* s_z = reinterpret_cast<float*>(lds + words + 2 * K);        // [K]
-
-  // the teacher's distribution: y_k = t_k c, p_k = 2^(y_k - max) / sum
-  float tmax = -INFINITY;
-  if (w != 0.0f) {
-    for (uint32_t i = t; i < words; i += nt) bits[i] = 0;
-    if (t == 0) s_dup = 0;
-    for (uint32_t k = t; k < K; k += nt) {
-      const uint64_t e = row * in.ld_top + k;
-      const int64_t id = in.index_bytes == 8 ? static_cast<const int64_t*>(in.top_index)[e]
-                                             : static_cast<const int32_t*>(in.top_index)[e];
-      const bool valid = id >= 0 && id < (int64_t)vocab;
-      const float y = valid ? load_as_float(in.top_logits, in.teacher_dtype, e) : -INFINITY;
-      s_idx[k] = valid ? (int)id : -1;
-      s_p[k] = y;
-      s_z[k] = valid ? (float)z[id] : -INFINITY;
-      tmax = y > tmax || y != y ? y : tmax;
-    }
-  }
-  // tail: log of a mass at temperature T, so it is compared as (tail * T) among the logits; kept
-  // apart as its own base-2 exponent
-  const float ytail = TAIL && w != 0.0f ? in.tail[row] * 1.44269504088896340736f : -INFINITY;
-  for (int o = 32; o; o >>= 1) {
-    const float x = __shfl_xor(tmax, o);
-    tmax = x > tmax || x != x ? x : tmax;
-  }
-  __syncthreads();
-  if (t % 64 == 0) s_f[t / 64] = tmax;
-  __syncthreads();
-  for (int i = 0; i < nt / 64; ++i) tmax = s_f[i] > tmax || s_f[i] != s_f[i] ? s_f[i] : tmax;
-  if (w == 0.0f || (tmax == -INFINITY && ytail == -INFINITY)) {
+  if (w == 0.0f) {
     if ((MODE & 1) && t == 0) {
       a.loss[row] = 0.0f;
       if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
     }
-    if (MODE & 2)
-      for (uint32_t v = t; v < vocab; v += nt) dz[v] = (T)0.0f;
+    if (MODE & 2) {
+      V zero = {};
+      for (uint32_t i = t; i < body; i += NT) *reinterpret_cast<V*>(dz + (uint64_t)i * W) = zero;
+      if (last < vocab) dz[last] = (T)0.0f;
+    }
     return;
   }
-  // exponents relative to the larger of the listed entries and the tail
-  const float listed_over_tail = mul_c(a, tmax) - ytail;  // +inf without a tail
-  const bool tail_first = listed_over_tail < 0.0f;
-  float tsum = 0.0f;
-  for (uint32_t k = t; k < K; k += nt) {
-    float y = s_p[k] == -INFINITY ? -INFINITY : mul_c(a, s_p[k] - tmax);
-    if (tail_first) y += listed_over_tail;
-    s_p[k] = y;
-    tsum += exp2f(y);
-    if (s_idx[k] >= 0) {
-      const uint32_t bit = 1u << (s_idx[k] & 31);
-      if (atomicOr(&bits[s_idx[k] >> 5], bit) & bit) s_dup = 1;
-    }
-  }
-  tsum = block_sum(tsum, s_f);
-  const float ytail_rel = tail_first ? 0.0f : -listed_over_tail;
-  const float etail = TAIL ? exp2f(ytail_rel) : 0.0f;
-  tsum += etail;
-  const float log_tsum = log2f(tsum), ptail = etail / tsum;
   __syncthreads();
+  if (wave == 0) teach<T, TAIL>(a, row, z, bits, s_idx, s_y, s_z, &teacher);
+  if (TAIL) __syncthreads();  // the sum needs to know what is listed
 
   // the student's (m, s): of every entry, or with a tail of the entries not listed
+  auto skip = [&](uint32_t i) -> uint32_t {
+    return TAIL ? bits[i * W / 32] >> (i * W % 32) : 0;  // W bits from bit 0
+  };
   MaxSum rest{kLowest, 0.0f};
   if (MODE & 1) {
-    const uint32_t body = vocab / W;
-    for (uint32_t i = t; i < body; i += nt) {
-      const V x = *reinterpret_cast<const V*>(z + (uint64_t)i * W);
+    auto one = [&](V x, uint32_t i) {
       float f[W];
+#pragma unroll
       for (int j = 0; j < W; ++j) f[j] = (float)x[j];
-      if (TAIL) {
-        const uint32_t mask = bits[i * W / 32] >> (i * W % 32);
-        for (int j = 0; j < W; ++j) f[j] = mask >> j & 1 ? -INFINITY : f[j];
+      add<T, W>(a, rest, f, skip(i));
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i * NT + t < (int)body) one(held[i], i * NT + t);
+    } else {
+      uint32_t i = t;
+      for (; i + 3 * NT < body; i += 4 * NT) {
+        V x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const V*>(z + (uint64_t)(i + u * NT) * W);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) one(x[u], i + u * NT);
       }
-      float m = f[0];
-      for (int j = 1; j < W; ++j) m = f[j] > m ? f[j] : m;
-      if (m > rest.m) {
-        rest.s *= exp2f(mul_c(a, rest.m - m));
-        rest.m = m;
-      }
-      float s = 0.0f;
-      for (int j = 0; j < W; ++j) s += __builtin_amdgcn_exp2f(mul_s<T>(a, f[j] - rest.m));
-      rest.s += s;
+      for (; i < body; i += NT) one(*reinterpret_cast<const V*>(z + (uint64_t)i * W), i);
     }
-    for (uint32_t v = body * W + t; v < vocab; v += nt) {
-      float f = (float)z[v];
-      if (TAIL && bits[v >> 5] >> (v & 31) & 1) f = -INFINITY;
-      if (f > rest.m) {
-        rest.s *= exp2f(mul_c(a, rest.m - f));
-        rest.m = f;
-      }
-      rest.s += __builtin_amdgcn_exp2f(mul_s<T>(a, f - rest.m));
+    if (last < vocab) {
+      float f[1] = {(float)z[last]};
+      add<T, 1>(a, rest, f, TAIL ? bits[last >> 5] >> (last & 31) : 0);
     }
-    block_join(a, rest, s_ms);
-    if (a.stats && t == 0) a.stats[2 * row] = rest.m, a.stats[2 * row + 1] = rest.s;
+    rest = wave_join(a, rest);
+    if ((t & 63) == 0) s_ms[wave] = rest;
   } else {
     rest.m = a.stats_in[2 * row], rest.s = a.stats_in[2 * row + 1];
   }
-
-  // Entries listed twice: the first of them (its leader) takes the sum of their p for the
-  // gradient and stands for them in the student's mass.
-  const bool dup = s_dup;
-  MaxSum all = rest;
-  if (TAIL) {
-    MaxSum top{kLowest, 0.0f};
-    for (uint32_t k = t; k < K; k += nt) {
-      bool leader = s_idx[k] >= 0;
-      if (dup && leader)
-        for (uint32_t j = 0; j < k; ++j) leader &= s_idx[j] != s_idx[k];
-      if (leader) top = join(a, top, MaxSum{s_z[k] > kLowest ? s_z[k] : kLowest, s_z[k] == -INFINITY ? 0.0f : 1.0f});
-      if (s_z[k] != s_z[k]) top.s = s_z[k];
+  __syncthreads();
+  if (teacher.none) {
+    if ((MODE & 1) && t == 0) {
+      a.loss[row] = 0.0f;
+      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
     }
-    block_join(a, top, s_ms);
-    all = join(a, rest, top);
+    if (MODE & 2) {
+      V zero = {};
+      for (uint32_t i = t; i < body; i += NT) *reinterpret_cast<V*>(dz + (uint64_t)i * W) = zero;
+      if (last < vocab) dz[last] = (T)0.0f;
+    }
+    return;
   }
-  const float bad = all.s > 0.0f ? 0.0f : NAN;   // no softmax: NaN, or nothing but -inf
-  const float log_s = log2f(all.s) + bad;
-  const float qrest = exp2f(mul_c(a, rest.m - all.m)) * rest.s / all.s;
-
   if (MODE & 1) {
+    rest = s_ms[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) rest = join(a, rest, s_ms[i]);
+    if (a.stats && t == 0) a.stats[2 * row] = rest.m, a.stats[2 * row + 1] = rest.s;
+  }
+  const MaxSum all = TAIL ? join(a, rest, teacher.top) : rest;
+  const float bad = all.s > 0.0f ? 0.0f : NAN;   // no softmax: NaN, or nothing but -inf
+  const float p_tail = teacher.p_tail;
+
+  if ((MODE & 1) && wave == 0) {
     // in natural logarithms: (z - m)/T stays finite where its base-2 form would overflow
-    const float ln_s = kLn2 * log_s;
+    const float ln_s = kLn2 * (log2f(all.s) + bad);
     float kl = 0.0f;
-    for (uint32_t k = t; k < K; k += nt) {
-      const float lp = s_p[k] - log_tsum, p = exp2f(lp);
+    for (uint32_t k = t; k < K; k += 64) {
+      const float lp = s_y[k] - teacher.log_sum, p = exp2f(lp);
       if (!(p == 0.0f)) kl += p * (kLn2 * lp - ((s_z[k] - all.m) * a.inv_t - ln_s));
     }
-    kl = block_sum(kl, s_f);
-    if (TAIL && ptail > 0.0f) {
+    kl = wave_sum(kl);
+    if (TAIL && !(p_tail == 0.0f)) {
       const float lq = rest.s == 0.0f
                            ? -INFINITY
                            : (rest.m - all.m) * a.inv_t + kLn2 * log2f(rest.s) - ln_s;
-      kl += ptail * (kLn2 * (ytail_rel - log_tsum) - lq);
+      kl += p_tail * (kLn2 * teacher.log_tail - lq);
     }
     if (t == 0) a.loss[row] = w * kl + bad;
   }
   if (MODE & 2) {
     const float g = a.scale * (a.upstream ? a.upstream[row] : 1.0f) * w * a.inv_t;
     const float inv = g / all.s;
-    const float fout = TAIL ? (rest.s == 0.0f ? bad : g * (qrest - ptail) / rest.s) : inv;
+    float fout = inv;
+    if (TAIL) {
+      const float q_rest = exp2f(mul_c(a, rest.m - all.m)) * rest.s / all.s;
+      fout = rest.s == 0.0f ? bad : g * (q_rest - p_tail) / rest.s;
+    }
     const float m = rest.m;
-    const uint32_t body = vocab / W;
-    for (uint32_t i = t; i < body; i += nt) {
-      const V x = *reinterpret_cast<const V*>(z + (uint64_t)i * W);
+    auto one = [&](V x, uint32_t i) {
       V y;
+#pragma unroll
       for (int j = 0; j < W; ++j) y[j] = (T)(fout * __builtin_amdgcn_exp2f(mul_s<T>(a, (float)x[j] - m)));
       *reinterpret_cast<V*>(dz + (uint64_t)i * W) = y;
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i * NT + t < (int)body) one(held[i], i * NT + t);
+    } else {
+      uint32_t i = t;
+      for (; i + 3 * NT < body; i += 4 * NT) {
+        V x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const V*>(z + (uint64_t)(i + u * NT) * W);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) one(x[u], i + u * NT);
+      }
+      for (; i < body; i += NT) one(*reinterpret_cast<const V*>(z + (uint64_t)i * W), i);
     }
-    for (uint32_t v = body * W + t; v < vocab; v += nt)
-      dz[v] = (T)(fout * __builtin_amdgcn_exp2f(mul_s<T>(a, (float)z[v] - m)));
+    if (last < vocab) dz[last] = (T)(fout * __builtin_amdgcn_exp2f(mul_s<T>(a, (float)z[last] - m)));
     __syncthreads();
-    for (uint32_t k = t; k < K; k += nt) {
+    // over the listed entries, one thread per index: entries of one index add their p, in order
+    for (uint32_t k = t; k < K; k += NT) {
       bool leader = s_idx[k] >= 0;
-      float p = exp2f(s_p[k] - log_tsum);
-      if (dup && leader) {
+      float p = exp2f(s_y[k] - teacher.log_sum);
+      if (teacher.dup && leader) {
         for (uint32_t j = 0; j < k; ++j) leader &= s_idx[j] != s_idx[k];
         for (uint32_t j = k + 1; j < K && leader; ++j)
-          if (s_idx[j] == s_idx[k]) p += exp2f(s_p[j] - log_tsum);
+          if (s_idx[j] == s_idx[k]) p += exp2f(s_y[j] - teacher.log_sum);
       }
       if (leader) dz[s_idx[k]] = (T)(inv * exp2f(mul_c(a, s_z[k] - all.m)) - g * p + bad);
     }
   }
 }
 
+template <typename T, bool TAIL, int MODE, int NV, int NT>
+hipError_t launch_one(const Args& a, hipStream_t s) {
+  const size_t lds = ((a.in.vocab + 127) / 128 * 4 + 3 * a.in.topk) * 4;
+  k_distill<T, TAIL, MODE, NV, NT><<<dim3((unsigned)a.in.rows), dim3(NT), lds, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T, bool TAIL>
 hipError_t launch(const Args& a, int mode, hipStream_t s) {
-  const uint64_t words = (a.in.vocab + 31) / 32 + 3 * a.in.topk;
-  const dim3 grid((unsigned)a.in.rows), block(256);
-  const size_t lds = words * 4;
-  if (mode == kForward) k_distill<T, TAIL, kForward><<<grid, block, lds, s>>>(a);
-  if (mode == kBackward) k_distill<T, TAIL, kBackward><<<grid, block, lds, s>>>(a);
-  if (mode == kStep) k_distill<T, TAIL, kStep><<<grid, block, lds, s>>>(a);
-  return hipGetLastError();
+  const uint64_t vectors = a.in.vocab / Pack<T>::n;
+  // few rows or long ones: a block of 1024 threads, which alone keeps more loads in flight
+  const bool wide = a.in.rows < 512 || vectors > 16 * 256;
+  if (mode == kForward)
+    return wide ? launch_one<T, TAIL, kForward, 0, 1024>(a, s) : launch_one<T, TAIL, kForward, 0, 256>(a, s);
+  if (mode == kBackward)
+    return wide ? launch_one<T, TAIL, kBackward, 0, 1024>(a, s)
+                : launch_one<T, TAIL, kBackward, 0, 256>(a, s);
+  if (vectors <= 4 * 256 && a.in.rows >= 512) return launch_one<T, TAIL, kStep, 4, 256>(a, s);
+  if (vectors <= 4 * 1024 && a.in.rows < 512) return launch_one<T, TAIL, kStep, 4, 1024>(a, s);
+  if (vectors <= 8 * 512) return launch_one<T, TAIL, kStep, 8, 512>(a, s);
+  if (vectors <= 8 * 1024) return launch_one<T, TAIL, kStep, 8, 1024>(a, s);
+  if (vectors <= 16 * 1024) return launch_one<T, TAIL, kStep, 16, 1024>(a, s);
+  return launch_one<T, TAIL, kStep, 0, 1024>(a, s);
 }
 
 struct Arr {
