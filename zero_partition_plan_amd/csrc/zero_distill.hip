@@ -60,11 +60,45 @@ struct MaxSum {
   float m, s;
 };
 
+// 2^x for x <= 0: the instruction itself (about one unit in the last place, 0 below 2^-126)
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+
 __device__ __forceinline__ MaxSum join(const Args& a, MaxSum x, MaxSum y) {
   MaxSum r;
   r.m = x.m > y.m ? x.m : y.m;
-  r.s = x.s * exp2f(mul_c(a, x.m - r.m)) + y.s * exp2f(mul_c(a, y.m - r.m));
+  r.s = x.s * ex2(mul_c(a, x.m - r.m)) + y.s * ex2(mul_c(a, y.m - r.m));
   return r;
+}
+
+// Reductions over a wave in a fixed order, by lane moves inside the vector unit: a row's latency is a
+// chain of them, and a move through LDS takes several times as long. The result is in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v, float none) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                               __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
+
+template <typename Op>
+__device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
+  v = op(v, moved<0x111, 0xf>(v, none));  // lanes 1, 2, 4, 8 before, in rows of 16
+  v = op(v, moved<0x112, 0xf>(v, none));
+  v = op(v, moved<0x114, 0xf>(v, none));
+  v = op(v, moved<0x118, 0xf>(v, none));
+  v = op(v, moved<0x142, 0xa>(v, none));  // a row's last lane to the next row
+  v = op(v, moved<0x143, 0xc>(v, none));  // lane 31 to the upper rows
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_reduce(v, 0.0f, [](float x, float y) { return x + y; });
+}
+
+// the larger, or a NaN if there is one
+__device__ __forceinline__ float larger(float x, float y) { return y > x || y != y ? y : x; }
+
+__device__ __forceinline__ MaxSum wave_join(const Args& a, MaxSum v) {
+  const float m = wave_reduce(v.m, kLowest, [](float x, float y) { return x > y ? x : y; });
+  return MaxSum{m, wave_sum(v.s * ex2(mul_c(a, v.m - m)))};
 }
 
 __device__ __forceinline__ float load_as_float(const void* p, int32_t dtype, uint64_t i) {
@@ -81,16 +115,6 @@ struct Pack {
   typedef vec type;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-__device__ __forceinline__ MaxSum wave_join(const Args& a, MaxSum v) {
-  for (int o = 32; o; o >>= 1) v = join(a, v, MaxSum{__shfl_xor(v.m, o), __shfl_xor(v.s, o)});
-  return v;
-}
-
 // What the first wave leaves for the others.
 struct Teacher {
   MaxSum top;       // the listed entries' logits, each index once (tail only)
@@ -101,30 +125,40 @@ struct Teacher {
   int none;         // no teacher mass
 };
 
-// The teacher's entries, by one wave: exponents s_y[k] (-inf: no mass), indices s_idx[k] (-1: no
+// An entry of the teacher as it lies in memory.
+struct Entry {
+  int64_t id;
+  float y;
+};
+
+__device__ __forceinline__ Entry load_entry(const zero_distill_in& in, uint64_t row, uint32_t k) {
+  const uint64_t e = row * in.ld_top + k;
+  Entry r;
+  r.id = in.index_bytes == 8 ? static_cast<const int64_t*>(in.top_index)[e]
+                             : static_cast<const int32_t*>(in.top_index)[e];
+  r.y = load_as_float(in.top_logits, in.teacher_dtype, e);
+  return r;
+}
+
+// The teacher's entries, by one wave (`first`: its lanes' first ones): exponents s_y[k] (-inf: no mass), indices s_idx[k] (-1: no
 // entry) and the student's logits there.
 template <typename T, bool TAIL>
-__device__ __forceinline__ void teach(const Args& a, uint64_t row, const T* z, uint32_t* bits, int* s_idx,
-                                      float* s_y, float* s_z, Teacher* out) {
+__device__ __forceinline__ void teach(const Args& a, uint64_t row, Entry first, const T* z, uint32_t* bits,
+                                      int* s_idx, float* s_y, float* s_z, Teacher* out) {
   const zero_distill_in& in = a.in;
   const uint32_t K = (uint32_t)in.topk;
   const int lane = threadIdx.x;
   float tmax = -INFINITY;
   for (uint32_t k = lane; k < K; k += 64) {
-    const uint64_t e = row * in.ld_top + k;
-    const int64_t id = in.index_bytes == 8 ? static_cast<const int64_t*>(in.top_index)[e]
-                                           : static_cast<const int32_t*>(in.top_index)[e];
-    const bool valid = id >= 0 && id < (int64_t)in.vocab;
-    const float y = valid ? load_as_float(in.top_logits, in.teacher_dtype, e) : -INFINITY;
-    s_idx[k] = valid ? (int)id : -1;
+    const Entry e = k < 64 ? first : load_entry(in, row, k);
+    const bool valid = e.id >= 0 && e.id < (int64_t)in.vocab;
+    const float y = valid ? e.y : -INFINITY;
+    s_idx[k] = valid ? (int)e.id : -1;
     s_y[k] = y;
-    s_z[k] = valid ? (float)z[id] : -INFINITY;
-    tmax = y > tmax || y != y ? y : tmax;
+    s_z[k] = valid ? (float)z[e.id] : -INFINITY;
+    tmax = larger(tmax, y);
   }
-  for (int o = 32; o; o >>= 1) {
-    const float x = __shfl_xor(tmax, o);
-    tmax = x > tmax || x != x ? x : tmax;
-  }
+  tmax = wave_reduce(tmax, -INFINITY, larger);
   // the tail is given as a logarithm at temperature T; exponents are relative to the larger of the
   // listed entries and the tail
   const float ytail = TAIL ? in.tail[row] * 1.44269504088896340736f : -INFINITY;
@@ -136,7 +170,7 @@ __device__ __forceinline__ void teach(const Args& a, uint64_t row, const T* z, u
     float y = s_y[k] == -INFINITY ? -INFINITY : mul_c(a, s_y[k] - tmax);
     if (tail_first) y += over;
     s_y[k] = y;
-    sum += exp2f(y);
+    sum += ex2(y);
     if (s_idx[k] >= 0) {
       const uint32_t bit = 1u << (s_idx[k] & 31);
       if (atomicOr(&bits[s_idx[k] >> 5], bit) & bit) dup = 1;
@@ -144,7 +178,7 @@ __device__ __forceinline__ void teach(const Args& a, uint64_t row, const T* z, u
   }
   dup = __any(dup);
   const float y_rel = tail_first ? 0.0f : -over;
-  const float e_tail = TAIL ? exp2f(y_rel) : 0.0f;
+  const float e_tail = TAIL ? ex2(y_rel) : 0.0f;
   sum = wave_sum(sum) + e_tail;
   MaxSum top{kLowest, 0.0f};
   if (TAIL) {
@@ -171,17 +205,19 @@ __device__ __forceinline__ void teach(const Args& a, uint64_t row, const T* z, u
 // Adds n values to a running sum; those whose bit in `skip` is set are left out.
 template <typename T, int N>
 __device__ __forceinline__ void add(const Args& a, MaxSum& r, float (&f)[N], uint32_t skip) {
+  if (skip & ((1u << N) - 1)) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) f[j] = skip >> j & 1 ? -INFINITY : f[j];
+    for (int j = 0; j < N; ++j) f[j] = skip >> j & 1 ? -INFINITY : f[j];
+  }
   float m = f[0];
 #pragma unroll
   for (int j = 1; j < N; ++j) m = f[j] > m ? f[j] : m;
   if (m > r.m) {
-    r.s *= exp2f(mul_c(a, r.m - m));
+    r.s *= ex2(mul_c(a, r.m - m));
     r.m = m;
   }
 #pragma unroll
-  for (int j = 0; j < N; ++j) r.s += __builtin_amdgcn_exp2f(mul_s<T>(a, f[j] - r.m));
+  for (int j = 0; j < N; ++j) r.s += ex2(mul_s<T>(a, f[j] - r.m));
 }
 
 // NV: 16-byte vectors of the row that a thread of the step holds in registers; 0: reads it again.
@@ -206,13 +242,16 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
   float* s_y = reinterpret_cast<float*>(lds + words + K);
   float* s_z = reinterpret_cast<float*>(lds + words + 2 * K);
 
+  // in the order of need: the row's weight, the teacher's entries, the row
+  const float w = in.weight ? in.weight[row] : 1.0f;
+  Entry first{-1, 0.0f};
+  if (t < 64 && t < (int)K) first = load_entry(in, row, t);
   V held[NV ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (i * NT + t < (int)body) held[i] = *reinterpret_cast<const V*>(z + (uint64_t)(i * NT + t) * W);
   for (uint32_t i = t; i < words / 4; i += NT)
     reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
-  const float w = in.weight ? in.weight[row] : 1.0f;
   if (w == 0.0f) {
     if ((MODE & 1) && t == 0) {
       a.loss[row] = 0.0f;
@@ -226,7 +265,7 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
     return;
   }
   __syncthreads();
-  if (wave == 0) teach<T, TAIL>(a, row, z, bits, s_idx, s_y, s_z, &teacher);
+  if (wave == 0) teach<T, TAIL>(a, row, first, z, bits, s_idx, s_y, s_z, &teacher);
   if (TAIL) __syncthreads();  // the sum needs to know what is listed
 
   // the student's (m, s): of every entry, or with a tail of the entries not listed
@@ -281,7 +320,10 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
   if (MODE & 1) {
     rest = s_ms[0];
 #pragma unroll
-    for (int i = 1; i < NT / 64; ++i) rest = join(a, rest, s_ms[i]);
+    for (int i = 1; i < NT / 64; ++i) rest.m = s_ms[i].m > rest.m ? s_ms[i].m : rest.m;
+    rest.s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) rest.s += s_ms[i].s * ex2(mul_c(a, s_ms[i].m - rest.m));
     if (a.stats && t == 0) a.stats[2 * row] = rest.m, a.stats[2 * row + 1] = rest.s;
   }
   const MaxSum all = TAIL ? join(a, rest, teacher.top) : rest;
@@ -293,7 +335,7 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
     const float ln_s = kLn2 * (log2f(all.s) + bad);
     float kl = 0.0f;
     for (uint32_t k = t; k < K; k += 64) {
-      const float lp = s_y[k] - teacher.log_sum, p = exp2f(lp);
+      const float lp = s_y[k] - teacher.log_sum, p = ex2(lp);
       if (!(p == 0.0f)) kl += p * (kLn2 * lp - ((s_z[k] - all.m) * a.inv_t - ln_s));
     }
     kl = wave_sum(kl);
@@ -310,14 +352,14 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
     const float inv = g / all.s;
     float fout = inv;
     if (TAIL) {
-      const float q_rest = exp2f(mul_c(a, rest.m - all.m)) * rest.s / all.s;
+      const float q_rest = ex2(mul_c(a, rest.m - all.m)) * rest.s / all.s;
       fout = rest.s == 0.0f ? bad : g * (q_rest - p_tail) / rest.s;
     }
     const float m = rest.m;
     auto one = [&](V x, uint32_t i) {
       V y;
 #pragma unroll
-      for (int j = 0; j < W; ++j) y[j] = (T)(fout * __builtin_amdgcn_exp2f(mul_s<T>(a, (float)x[j] - m)));
+      for (int j = 0; j < W; ++j) y[j] = (T)(fout * ex2(mul_s<T>(a, (float)x[j] - m)));
       *reinterpret_cast<V*>(dz + (uint64_t)i * W) = y;
     };
     if constexpr (NV > 0) {
@@ -335,18 +377,18 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
       }
       for (; i < body; i += NT) one(*reinterpret_cast<const V*>(z + (uint64_t)i * W), i);
     }
-    if (last < vocab) dz[last] = (T)(fout * __builtin_amdgcn_exp2f(mul_s<T>(a, (float)z[last] - m)));
+    if (last < vocab) dz[last] = (T)(fout * ex2(mul_s<T>(a, (float)z[last] - m)));
     __syncthreads();
     // over the listed entries, one thread per index: entries of one index add their p, in order
     for (uint32_t k = t; k < K; k += NT) {
       bool leader = s_idx[k] >= 0;
-      float p = exp2f(s_y[k] - teacher.log_sum);
+      float p = ex2(s_y[k] - teacher.log_sum);
       if (teacher.dup && leader) {
         for (uint32_t j = 0; j < k; ++j) leader &= s_idx[j] != s_idx[k];
         for (uint32_t j = k + 1; j < K && leader; ++j)
-          if (s_idx[j] == s_idx[k]) p += exp2f(s_y[j] - teacher.log_sum);
+          if (s_idx[j] == s_idx[k]) p += ex2(s_y[j] - teacher.log_sum);
       }
-      if (leader) dz[s_idx[k]] = (T)(inv * exp2f(mul_c(a, s_z[k] - all.m)) - g * p + bad);
+      if (leader) dz[s_idx[k]] = (T)(inv * ex2(mul_c(a, s_z[k] - all.m)) - g * p + bad);
     }
   }
 }
@@ -360,20 +402,34 @@ hipError_t launch_one(const Args& a, hipStream_t s) {
 
 template <typename T, bool TAIL>
 hipError_t launch(const Args& a, int mode, hipStream_t s) {
-  const uint64_t vectors = a.in.vocab / Pack<T>::n;
-  // few rows or long ones: a block of 1024 threads, which alone keeps more loads in flight
-  const bool wide = a.in.rows < 512 || vectors > 16 * 256;
-  if (mode == kForward)
-    return wide ? launch_one<T, TAIL, kForward, 0, 1024>(a, s) : launch_one<T, TAIL, kForward, 0, 256>(a, s);
-  if (mode == kBackward)
-    return wide ? launch_one<T, TAIL, kBackward, 0, 1024>(a, s)
-                : launch_one<T, TAIL, kBackward, 0, 256>(a, s);
-  if (vectors <= 4 * 256 && a.in.rows >= 512) return launch_one<T, TAIL, kStep, 4, 256>(a, s);
-  if (vectors <= 4 * 1024 && a.in.rows < 512) return launch_one<T, TAIL, kStep, 4, 1024>(a, s);
-  if (vectors <= 8 * 512) return launch_one<T, TAIL, kStep, 8, 512>(a, s);
-  if (vectors <= 8 * 1024) return launch_one<T, TAIL, kStep, 8, 1024>(a, s);
-  if (vectors <= 16 * 1024) return launch_one<T, TAIL, kStep, 16, 1024>(a, s);
-  return launch_one<T, TAIL, kStep, 0, 1024>(a, s);
+  const uint64_t v = a.in.vocab / Pack<T>::n;  // vectors of a row
+#define ZERO_GO(MODE, NV, NT) return launch_one<T, TAIL, MODE, NV, NT>(a, s)
+  // Few rows: 1024 threads on each, for the latency of one. Many: small blocks, several to a CU, so
+  // that one's loads run under another's arithmetic and stores (8192 x 32000 bf16).
+  const bool wide = a.in.rows < 512;
+  if (mode == kForward) {
+    if (wide) ZERO_GO(kForward, 0, 1024);
+    if (v > 4096) ZERO_GO(kForward, 0, 512);
+    ZERO_GO(kForward, 0, 256);
+  }
+  if (mode == kBackward) {
+    if (wide) ZERO_GO(kBackward, 0, 1024);
+    if (v > 4096) ZERO_GO(kBackward, 0, 512);
+    ZERO_GO(kBackward, 0, 256);
+  }
+  if (wide) {
+    if (v <= 4 * 1024) ZERO_GO(kStep, 4, 1024);
+    if (v <= 8 * 1024) ZERO_GO(kStep, 8, 1024);
+  } else {
+    if (v <= 4 * 256) ZERO_GO(kStep, 4, 256);
+    if (v <= 8 * 256) ZERO_GO(kStep, 8, 256);
+    if (v <= 16 * 256) ZERO_GO(kStep, 16, 256);
+    if (v <= 28 * 256) ZERO_GO(kStep, 28, 256);
+    if (v <= 28 * 512) ZERO_GO(kStep, 28, 512);
+  }
+  if (v <= 16 * 1024) ZERO_GO(kStep, 16, 1024);
+  ZERO_GO(kStep, 0, 1024);
+#undef ZERO_GO
 }
 
 struct Arr {
