@@ -80,93 +80,134 @@ __device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt
   }
 }
 
-// z -> out for up to 8 neighbouring columns n.. of row m (fewer at the right edge). The activation
-// stands once for both kinds of row; vectors may lie at any element.
-template <typename T>
-__device__ __forceinline__ void finish_row(const GemmDev& g, float* z, uint64_t m, uint32_t n) {
+// z -> out for 8 neighbouring columns from n of R rows: m, m + dm, ... Everything that is read is asked
+// for before it is needed, and the R rows' arithmetic stands side by side, as nothing else hides
+// its latency. The activation is chosen once for all of them. Vectors may lie at any element.
+template <typename T, int R>
+__device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], uint64_t m, uint32_t dm,
+                                            uint32_t n) {
   typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
   typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
-  const T* bias = static_cast<const T*>(g.bias) + n;
   const T* res = static_cast<const T*>(g.res) + m * g.ldr + n;
   T* pre = static_cast<T*>(g.pre) + m * g.ldp + n;
   float* out32 = static_cast<float*>(g.out) + m * g.ldo + n;
   T* out16 = static_cast<T*>(g.out) + m * g.ldo + n;
-  if (n + 8 <= g.n) {
-    if (g.bias) {
-      const v8 b = *reinterpret_cast<const v8*>(bias);
+  auto there = [&](int r) { return m + (uint64_t)r * dm < g.m; };
+  v8 held[R];
+  if (g.res) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += (float)b[j];
-    }
-    if (g.pre) {
-      v8 o;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
-      *reinterpret_cast<v8*>(pre) = o;
-    }
-    act_rt<8>(z, g.act);
-    if (g.res) {
-      const v8 r = *reinterpret_cast<const v8*>(res);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] += (float)r[j];
-    }
-    if (g.out_f32) {
-      f8 o;
-      if (g.accumulate) {
-        o = *reinterpret_cast<f8*>(out32);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] += o[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = z[j];
-      *reinterpret_cast<f8*>(out32) = o;
-    } else {
-      v8 o;
-      if (g.accumulate) {
-        o = *reinterpret_cast<v8*>(out16);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] += (float)o[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (T)z[j];
-      *reinterpret_cast<v8*>(out16) = o;
-    }
-    return;
+    for (int r = 0; r < R; ++r)
+      if (there(r)) held[r] = *reinterpret_cast<const v8*>(res + (uint64_t)r * dm * g.ldr);
   }
-  const uint32_t left = g.n - n;
+  if (g.bias) {
+    const v8 b = *reinterpret_cast<const v8*>(static_cast<const T*>(g.bias) + n);
 #pragma unroll
-  for (int j = 0; j < 7; ++j) {
-    if (j >= (int)left) break;
-    float v[1] = {z[j]};
-    if (g.bias) v[0] += (float)bias[j];
-    if (g.pre) pre[j] = (T)v[0];
-    if (g.act) act_rt<1>(v, g.act);
-    if (g.res) v[0] += (float)res[j];
-    if (g.out_f32) {
-      out32[j] = g.accumulate ? v[0] + out32[j] : v[0];
-    } else {
-      out16[j] = (T)(g.accumulate ? v[0] + (float)out16[j] : v[0]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[r][j] += (float)b[j];
+  }
+  if (g.pre) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (T)z[r][j];
+      if (there(r)) *reinterpret_cast<v8*>(pre + (uint64_t)r * dm * g.ldp) = o;
+    }
+  }
+  act_rt<R * 8>(&z[0][0], g.act);
+  if (g.res) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[r][j] += (float)held[r][j];
+  }
+  if (g.out_f32) {
+    if (g.accumulate) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (there(r)) {
+          const f8 o = *reinterpret_cast<const f8*>(out32 + (uint64_t)r * dm * g.ldo);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[r][j] += o[j];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = z[r][j];
+      if (there(r)) *reinterpret_cast<f8*>(out32 + (uint64_t)r * dm * g.ldo) = o;
+    }
+  } else {
+    if (g.accumulate) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (there(r)) {
+          const v8 o = *reinterpret_cast<const v8*>(out16 + (uint64_t)r * dm * g.ldo);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[r][j] += (float)o[j];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (T)z[r][j];
+      if (there(r)) *reinterpret_cast<v8*>(out16 + (uint64_t)r * dm * g.ldo) = o;
     }
   }
 }
 
+// The same for one element, at the right edge.
 template <typename T>
-__device__ __forceinline__ void finish(const GemmDev& g, float* z, uint64_t m, uint32_t n) {
-  if (g.splits > 1) {
-    typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
-    float* w = g.ws + ((uint64_t)blockIdx.y * g.m + m) * g.n + n;
+__device__ __forceinline__ void finish_one(const GemmDev& g, float z, uint64_t m, uint32_t n) {
+  if (g.bias) z += (float)static_cast<const T*>(g.bias)[n];
+  if (g.pre) static_cast<T*>(g.pre)[m * g.ldp + n] = (T)z;
+  act_rt<1>(&z, g.act);
+  if (g.res) z += (float)static_cast<const T*>(g.res)[m * g.ldr + n];
+  if (g.out_f32) {
+    float* out = static_cast<float*>(g.out) + m * g.ldo + n;
+    *out = g.accumulate ? z + *out : z;
+  } else {
+    T* out = static_cast<T*>(g.out) + m * g.ldo + n;
+    *out = (T)(g.accumulate ? z + (float)*out : z);
+  }
+}
+
+// One row's up to 8 columns from n.
+template <typename T>
+__device__ __forceinline__ void finish_row(const GemmDev& g, float (&z)[1][8], uint64_t m, uint32_t n) {
+  if (n + 8 <= g.n) {
+    finish_rows<T, 1>(g, z, m, 1, n);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (n + j < g.n) finish_one<T>(g, z[0][j], m, n + j);
+}
+
+// Partial sums to the workspace, for the split's join.
+template <int R>
+__device__ __forceinline__ void keep_rows(const GemmDev& g, float (&z)[R][8], uint64_t m, uint32_t dm,
+                                          uint32_t n) {
+  typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint64_t row = m + (uint64_t)r * dm;
+    if (row >= g.m) continue;
+    float* w = g.ws + ((uint64_t)blockIdx.y * g.m + row) * g.n + n;
     if (n + 8 <= g.n) {
       f8 o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = z[j];
+      for (int j = 0; j < 8; ++j) o[j] = z[r][j];
       *reinterpret_cast<f8*>(w) = o;
     } else {
 #pragma unroll
       for (int j = 0; j < 7; ++j)
-        if (n + j < g.n) w[j] = z[j];
+        if (n + j < g.n) w[j] = z[r][j];
     }
-    return;
   }
-  finish_row<T>(g, z, m, n);
 }
 
 }  // namespace zero

@@ -16,17 +16,17 @@ __global__ __launch_bounds__(256) void k_join(GemmDev g) {
     const uint64_t m = i / groups;
     const uint32_t n = (uint32_t)(i % groups) * 8;
     typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
-    float z[8] = {};
+    float z[1][8] = {};
     for (uint32_t s = 0; s < g.splits; ++s) {
       const float* w = g.ws + ((uint64_t)s * g.m + m) * g.n + n;
       if (n + 8 <= g.n) {
         const f8 v = *reinterpret_cast<const f8*>(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] += v[j];
+        for (int j = 0; j < 8; ++j) z[0][j] += v[j];
       } else {
 #pragma unroll
         for (int j = 0; j < 7; ++j)
-          if (n + j < g.n) z[j] += w[j];
+          if (n + j < g.n) z[0][j] += w[j];
       }
     }
     finish_row<T>(g, z, m, n);
@@ -110,9 +110,9 @@ __global__ __launch_bounds__(1024) void k_few(GemmDev g) {
   __syncthreads();
   const uint32_t m = threadIdx.x >> 1, nn = n0 + (threadIdx.x & 1) * 8;
   if (m < MT * 16 && m < g.m && nn < g.n) {
-    float z[8];
+    float z[1][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = red[0][m][(threadIdx.x & 1) * 8 + j];
+    for (int j = 0; j < 8; ++j) z[0][j] = red[0][m][(threadIdx.x & 1) * 8 + j];
     finish_row<T>(g, z, m, nn);
   }
 #endif

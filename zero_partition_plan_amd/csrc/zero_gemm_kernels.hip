@@ -317,14 +317,30 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
                             acc[c][j][q * 4 + 3]);
       }
     __builtin_amdgcn_wave_barrier();
+    // two rows of a lane at a time: more in flight would spill the 256 x 256 tile's sums
+    constexpr int kPer = 64 / kLanes, R = 2;
 #pragma unroll 1
-    for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
-      const uint32_t m = m0 + wm0 + i * 32 + r, n = n0 + wn0 + (lane % kLanes) * 8;
-      const float* at = stage + r * kRow + (lane % kLanes) * 8;
-      float z[8];
-      *reinterpret_cast<float4*>(z) = *reinterpret_cast<const float4*>(at);
-      *reinterpret_cast<float4*>(z + 4) = *reinterpret_cast<const float4*>(at + 4);
-      if (m < g.m && n < g.n) finish<T>(g, z, m, n);
+    for (int r0 = lane / kLanes; r0 < 32; r0 += R * kPer) {
+      const uint32_t m = m0 + wm0 + i * 32 + r0, n = n0 + wn0 + (lane % kLanes) * 8;
+      const float* at = stage + r0 * kRow + (lane % kLanes) * 8;
+      float z[R][8];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        *reinterpret_cast<float4*>(&z[r][0]) = *reinterpret_cast<const float4*>(at + r * kPer * kRow);
+        *reinterpret_cast<float4*>(&z[r][4]) = *reinterpret_cast<const float4*>(at + r * kPer * kRow + 4);
+      }
+      if (m >= g.m || n >= g.n) continue;
+      if (g.splits > 1) {
+        keep_rows<R>(g, z, m, kPer, n);
+      } else if (n + 8 <= g.n) {
+        finish_rows<T, R>(g, z, m, kPer, n);
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < R; ++r)
+#pragma unroll 1
+          for (int j = 0; n + j < g.n; ++j)
+            if (m + r * kPer < g.m) finish_one<T>(g, at[r * kPer * kRow + j], m + r * kPer, n + j);
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
