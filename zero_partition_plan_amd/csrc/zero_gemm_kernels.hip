@@ -26,16 +26,16 @@ constexpr bool kAK = ZERO_GEMM_AK, kBK = ZERO_GEMM_BK;
 typedef T t8 __attribute__((ext_vector_type(8)));
 typedef T t4 __attribute__((ext_vector_type(4)));
 typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
-typedef float f16v __attribute__((ext_vector_type(16)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = kGemmStep;
 constexpr int kStages = 2;  // LDS stages
 
-[[maybe_unused]] __device__ __forceinline__ f16v mfma(t8 a, t8 b, f16v c) {
+[[maybe_unused]] __device__ __forceinline__ f4 mfma(t8 a, t8 b, f4 c) {
 #if ZERO_GEMM_DT == 2
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 #else
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 #endif
 }
 
@@ -60,7 +60,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 // the LDS answers 16 lanes of a 16-byte read at once from 256 bytes of banks, and 16 neighbouring
 // rows' chunks of one k then lie in its 16 different places.
 // k-major operand: 64 rows of R elements, the 32-byte granule g of row k at place g ^ swz(k): a
-// transposing read takes 32 lanes at once, 4 k of 2 neighbouring granules, again 256 bytes apart.
+// transposing read takes 32 lanes at once, 4 and 4 k (8 apart) of one granule, again in 256 bytes' different places.
 template <bool KM, int R, int NT>
 struct Tile {
   static constexpr int kChunks = R * kStepK / 8;
@@ -70,7 +70,8 @@ struct Tile {
 
   static __device__ __forceinline__ int swz(int k) {
     static_assert(R % 128 == 0 || R == 64 || R == 32, "whole granules, apart in 256 bytes");
-    return R % 128 == 0 ? (k & 3) << 1 : R == 64 ? k & 2 : 0;
+    const int half = k >> 3 & 1;
+    return R % 128 == 0 ? (k & 3) << 1 | half : R == 64 ? (k & 2) | half : half;
   }
 
   // (row, k) of the chunk that lies at place q of the tile
@@ -134,17 +135,16 @@ struct Tile {
     for (int r = 0; r < kRounds; ++r) *reinterpret_cast<t8*>(lds + (r * NT + tid) * 8) = held[r];
   }
 
-  // Fragment for 32 rows from row0 and 16 k from kk*16, read from LDS.
+  // Fragment for 16 rows from row0 and 32 k from kk*32, read from LDS.
   static __device__ __forceinline__ t8 frag(const T* lds, int row0, int kk, int lane) {
     if constexpr (!KM) {
-      const int row = row0 + (lane & 31);
-      const int c = (kk * 2 + (lane >> 5)) ^ (lane >> 1 & 7);
+      const int row = row0 + (lane & 15);
+      const int c = (kk * 4 + (lane >> 4)) ^ (lane >> 1 & 7);
       return *reinterpret_cast<const t8*>(lds + row * kStepK + c * 8);
     } else {
-      const int g = lane >> 4, i = lane & 15;
-      const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
-      const int gran = (row0 >> 4) + (g & 1);
-      const T* p = lds + k * R + ((gran ^ swz(k)) << 4) + (i & 3) * 4;
+      const int i = lane & 15;
+      const int k = kk * 32 + (lane >> 4) * 8 + (i >> 2);
+      const T* p = lds + k * R + (((row0 >> 4) ^ swz(k)) << 4) + (i & 3) * 4;
       const t4 lo = read_tr(p), hi = read_tr(p + 4 * R);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
@@ -156,7 +156,7 @@ struct Tile {
 template <int BM, int BN, int WM, int WN>
 struct Shape {
   static constexpr int NT = WM * WN * 64;
-  static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   using A = Tile<kAK, BM, NT>;
   using B = Tile<kBK, BN, NT>;
   static constexpr int kB = kStages * A::kElems;
@@ -166,21 +166,29 @@ struct Shape {
 template <typename S>
 struct Frags {
   t8 a[S::TM], b[S::TN];
-  __device__ __forceinline__ void load(const T* sa, const T* sb, int kk, int wm0, int wn0, int lane) {
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j) b[j] = S::B::frag(sb, wn0 + j * 32, kk, lane);
-#pragma unroll
-    for (int i = 0; i < S::TM; ++i) a[i] = S::A::frag(sa, wm0 + i * 32, kk, lane);
-  }
-  __device__ __forceinline__ void mul(f16v (&acc)[S::TM][S::TN]) const {
-#pragma unroll
-    for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j) acc[i][j] = mfma(b[j], a[i], acc[i][j]);
-  }
 };
 
-// From the last quarter of one step to the third of the next. On entry f holds the last
+// The products of the fragments in hand, 32 k, and in their places those of the 32 k after: a row
+// fragment is read again as soon as its products are issued, so one set of them is enough; the
+// column fragments, used to the end, take a second set.
+template <typename S>
+__device__ __forceinline__ void half(const T* sa, const T* sb, int kk, Frags<S>& f, f4 (&acc)[S::TM][S::TN],
+                                     int wm0, int wn0, int lane) {
+  t8 b[S::TN];
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) acc[i][j] = mfma(f.b[j], f.a[i], acc[i][j]);
+    f.a[i] = S::A::frag(sa, wm0 + i * 16, kk, lane);
+#pragma unroll
+    for (int j = i * S::TN / S::TM; j < (i + 1) * S::TN / S::TM; ++j)
+      b[j] = S::B::frag(sb, wn0 + j * 16, kk, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) f.b[j] = b[j];
+}
+
+// From the second half of one step to the first of the next. On entry f holds the last
 // fragments of the stage at da and db, which no wave reads any more: the loads of the step after
 // the next go there, while the products run through the stage at sa and sb. The stages are declared
 // apart, so that the reads of one need not wait for what is on its way into the other.
@@ -188,36 +196,27 @@ template <typename S, bool DIRECT>
 __device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restrict__ sb,
                                      T* __restrict__ da, T* __restrict__ db, const typename S::A& ta,
                                      const typename S::B& tb, const T* pa, uint32_t abytes, const T* pb,
-                                     uint32_t bbytes, int k_left, Frags<S>& f, f16v (&acc)[S::TM][S::TN],
+                                     uint32_t bbytes, int k_left, Frags<S>& f, f4 (&acc)[S::TM][S::TN],
                                      int wm0, int wn0, int wave, int lane) {
-  Frags<S> h;
   if (DIRECT) {
     ta.dma(pa, abytes, k_left, da, wave);
     tb.dma(pb, bbytes, k_left, db, wave);
   }
-  h.load(sa, sb, 0, wm0, wn0, lane);
-  f.mul(acc);
-  f.load(sa, sb, 1, wm0, wn0, lane);
-  h.mul(acc);
-  h.load(sa, sb, 2, wm0, wn0, lane);
-  f.mul(acc);
-  f.load(sa, sb, 3, wm0, wn0, lane);
-  h.mul(acc);
-  // behind each matrix instruction its share of the LDS reads of the next quarter, and of the loads
-  constexpr int reads = (S::TM * (kAK ? 2 : 1) + S::TN * (kBK ? 2 : 1));
-  constexpr int muls = S::TM * S::TN;
-  constexpr int per = (reads + muls - 1) / muls;
-  constexpr int loads = (S::A::kRounds + S::B::kRounds + muls - 1) / muls;
+  half<S>(sa, sb, 0, f, acc, wm0, wn0, lane);
+  half<S>(sa, sb, 1, f, acc, wm0, wn0, lane);
+  // behind each row of matrix instructions its share of the LDS reads, and of the loads
+  constexpr int reads = (S::TM * (kAK ? 2 : 1) + S::TN * (kBK ? 2 : 1) + S::TM - 1) / S::TM;
+  constexpr int loads = (S::A::kRounds + S::B::kRounds + S::TM - 1) / S::TM;
 #pragma unroll
-  for (int i = 0; i < muls; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+  for (int i = 0; i < S::TM; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, S::TN, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
     __builtin_amdgcn_sched_group_barrier(0x20, loads, 0);
   }
 #pragma unroll
-  for (int i = 0; i < 3 * muls; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+  for (int i = 0; i < S::TM; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, S::TN, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
   }
 }
 
@@ -244,7 +243,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   Cursor<T, kAK, BM> ca(g.a, g.lda, m0, g.m, k_begin);
   Cursor<T, kBK, BN> cb(g.b, g.ldb, n0, g.n, k_begin);
 
-  f16v acc[S::TM][S::TN] = {};
+  f4 acc[S::TM][S::TN] = {};
   const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
   int k_left = (int)(g.k - k_begin);
   // k's last, partial chunk of a k-contiguous row comes with what lies behind the row
@@ -294,27 +293,26 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     body(Int<0>{}, s + 1 == steps);
     if (s + 1 < steps) body(Int<1>{}, s + 2 == steps);
   }
-  f.mul(acc);
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) acc[i][j] = mfma(f.b[j], f.a[i], acc[i][j]);
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // the last step's loads past the end land before LDS is reused
   __syncthreads();
   // 32 rows at a time through LDS: the matrix instruction leaves a lane 4 neighbouring columns of
   // one row; the epilogue wants 8 columns a lane, and a row's lanes side by side. One copy of its
   // code for all (it would be the larger part of the kernel, fetched cold by every launch).
-  constexpr int kRow = S::TN * 32 + 4;
-  constexpr int kLanes = S::TN * 32 / 8;  // lanes on a row
+  constexpr int kRow = S::TN * 16 + 4;
+  constexpr int kLanes = S::TN * 16 / 8;  // lanes on a row
   float* stage = reinterpret_cast<float*>(smem) + wave * (32 * kRow);
 #pragma unroll 1
-  for (int i = 0; i < S::TM; ++i) {
+  for (int i = 0; i < S::TM / 2; ++i) {
 #pragma unroll
     for (int c = 0; c < S::TM; ++c)
-      if (c == i) {
+      if (c / 2 == i) {
 #pragma unroll
         for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(stage + (lane & 31) * kRow + j * 32 + q * 8 + (lane >> 5) * 4) =
-                make_float4(acc[c][j][q * 4], acc[c][j][q * 4 + 1], acc[c][j][q * 4 + 2],
-                            acc[c][j][q * 4 + 3]);
+          *reinterpret_cast<f4*>(stage + (c % 2 * 16 + (lane & 15)) * kRow + j * 16 + (lane >> 4) * 4) = acc[c][j];
       }
     __builtin_amdgcn_wave_barrier();
     // two rows of a lane at a time: more in flight would spill the 256 x 256 tile's sums
@@ -352,7 +350,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
 template <bool DIRECT, int BM, int BN, int WM, int WN>
 hipError_t launch(const GemmDev& g, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
-  constexpr int epi = WM * WN * 32 * (S::TN * 32 + 4) * 4;
+  constexpr int epi = WM * WN * 32 * (S::TN * 16 + 4) * 4;
   constexpr int lds = S::kElems * 2 > epi ? S::kElems * 2 : epi;
   auto fn = k_gemm<S, DIRECT, BM, BN, WM, WN>;
   if (lds > 64 * 1024) {
