@@ -99,16 +99,22 @@ struct Tile {
     }
   }
 
+  // From the step on whose k end within it (k_left of them): chunks past the end read zeros.
+  __device__ __forceinline__ void clip(int k_left) {
+    if (KM || k0 < k_left) return;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) voff[r] = 0xfffffff0u;
+  }
+
   // Straight to LDS: `base` is the address of (first row, first k of this step), `bytes` what
-  // lies behind it; a load past that gives 0. k_left: k from the step's first to the end.
-  __device__ __forceinline__ void dma(const T* base, uint32_t bytes, int k_left, T* lds, int wave) const {
+  // lies behind it; a load past that gives 0.
+  __device__ __forceinline__ void dma(const T* base, uint32_t bytes, T* lds, int wave) const {
     auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
-    const bool past = !KM && k0 >= k_left;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (__attribute__((address_space(3))) void*)(lds + (r * NT + wave * 64) * 8), 16,
-          past ? 0xfffffff0u : voff[r], 0, 0, 0);
+          voff[r], 0, 0, 0);
   }
 
   // By way of registers, for operands off the 16 bytes that the direct loads need: chunks at any
@@ -196,11 +202,11 @@ template <typename S, bool DIRECT>
 __device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restrict__ sb,
                                      T* __restrict__ da, T* __restrict__ db, const typename S::A& ta,
                                      const typename S::B& tb, const T* pa, uint32_t abytes, const T* pb,
-                                     uint32_t bbytes, int k_left, Frags<S>& f, f4 (&acc)[S::TM][S::TN],
+                                     uint32_t bbytes, Frags<S>& f, f4 (&acc)[S::TM][S::TN],
                                      int wm0, int wn0, int wave, int lane) {
   if (DIRECT) {
-    ta.dma(pa, abytes, k_left, da, wave);
-    tb.dma(pb, bbytes, k_left, db, wave);
+    ta.dma(pa, abytes, da, wave);
+    tb.dma(pb, bbytes, db, wave);
   }
   half<S>(sa, sb, 0, f, acc, wm0, wn0, lane);
   half<S>(sa, sb, 1, f, acc, wm0, wn0, lane);
@@ -252,8 +258,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   Frags<S> f = {};
   if (steps > 0) {
     if (DIRECT) {
-      ta.dma(ca.p, ca.bytes(k_left), k_left, lds, wave);
-      tb.dma(cb.p, cb.bytes(k_left), k_left, lds + S::kB, wave);
+      if (k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
+      ta.dma(ca.p, ca.bytes(k_left), lds, wave);
+      tb.dma(cb.p, cb.bytes(k_left), lds + S::kB, wave);
     } else {
       ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
       tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
@@ -268,6 +275,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     cb.advance();
     k_left -= kStepK;
     const uint32_t abytes = ca.bytes(k_left), bbytes = cb.bytes(k_left);
+    if (DIRECT && k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
     // what the next stage needs has landed, and this wave's reads of the stage that is to be loaded
     // over are done: the barrier makes both true of all waves
     __builtin_amdgcn_s_waitcnt(kWaitAll);
@@ -282,8 +290,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
       ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
       tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
     }
-    step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, k_left, f, acc, wm0, wn0, wave,
-                    lane);
+    step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, f, acc, wm0, wn0, wave, lane);
     if (!DIRECT) {
       ta.put(da, tid);
       tb.put(db, tid);
