@@ -11,15 +11,18 @@ namespace zero {
 
 constexpr uint32_t kGemmStep = 64;  // k per LDS stage; splits of k are whole stages
 
-// Tile shapes: rows, columns, waves along the rows, waves along the columns.
-#define ZERO_GEMM_SHAPES        \
-  ZERO_SHAPE(0, 256, 256, 2, 4) \
-  ZERO_SHAPE(1, 128, 256, 2, 4) \
-  ZERO_SHAPE(2, 256, 128, 4, 2) \
-  ZERO_SHAPE(3, 128, 128, 2, 2) \
-  ZERO_SHAPE(4, 64, 256, 1, 4)  \
-  ZERO_SHAPE(5, 32, 256, 1, 4)  \
-  ZERO_SHAPE(6, 64, 64, 2, 2)
+// Tile shapes: number, whether operands off 16 bytes may take it, rows, columns, waves along the rows,
+// waves along the columns.
+#define ZERO_GEMM_SHAPES               \
+  ZERO_SHAPE(0, false, 256, 256, 2, 4) \
+  ZERO_SHAPE(1, true, 128, 256, 2, 4)  \
+  ZERO_SHAPE(2, true, 256, 128, 4, 2)  \
+  ZERO_SHAPE(3, true, 128, 128, 2, 2)  \
+  ZERO_SHAPE(4, true, 64, 256, 1, 4)   \
+  ZERO_SHAPE(5, true, 32, 256, 1, 4)   \
+  ZERO_SHAPE(6, true, 64, 64, 2, 2)    \
+  ZERO_SHAPE(7, false, 256, 192, 2, 4) \
+  ZERO_SHAPE(8, false, 192, 256, 2, 4)
 
 struct GemmDev {
   const void *a, *b, *bias, *res;
@@ -80,19 +83,19 @@ __device__ __forceinline__ void zero_partial(T* lds, int k_left, int tid, int nt
   }
 }
 
-// z -> out for 8 neighbouring columns from n of R rows: m, m + dm, ... Everything that is read is asked
+// z -> out for 8 neighbouring columns from n of R rows: m, m + dm, ... below m_end. Everything that is read is asked
 // for before it is needed, and the R rows' arithmetic stands side by side, as nothing else hides
 // its latency. The activation is chosen once for all of them. Vectors may lie at any element.
 template <typename T, int R>
 __device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], uint64_t m, uint32_t dm,
-                                            uint32_t n) {
+                                            uint32_t m_end, uint32_t n) {
   typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
   typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
   const T* res = static_cast<const T*>(g.res) + m * g.ldr + n;
   T* pre = static_cast<T*>(g.pre) + m * g.ldp + n;
   float* out32 = static_cast<float*>(g.out) + m * g.ldo + n;
   T* out16 = static_cast<T*>(g.out) + m * g.ldo + n;
-  auto there = [&](int r) { return m + (uint64_t)r * dm < g.m; };
+  auto there = [&](int r) { return m + (uint64_t)r * dm < m_end; };
   v8 held[R];
   if (g.res) {
 #pragma unroll
@@ -179,7 +182,7 @@ __device__ __forceinline__ void finish_one(const GemmDev& g, float z, uint64_t m
 template <typename T>
 __device__ __forceinline__ void finish_row(const GemmDev& g, float (&z)[1][8], uint64_t m, uint32_t n) {
   if (n + 8 <= g.n) {
-    finish_rows<T, 1>(g, z, m, 1, n);
+    finish_rows<T, 1>(g, z, m, 1, g.m, n);
     return;
   }
 #pragma unroll
@@ -190,12 +193,12 @@ __device__ __forceinline__ void finish_row(const GemmDev& g, float (&z)[1][8], u
 // Partial sums to the workspace, for the split's join.
 template <int R>
 __device__ __forceinline__ void keep_rows(const GemmDev& g, float (&z)[R][8], uint64_t m, uint32_t dm,
-                                          uint32_t n) {
+                                          uint32_t m_end, uint32_t n) {
   typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const uint64_t row = m + (uint64_t)r * dm;
-    if (row >= g.m) continue;
+    if (row >= m_end) continue;
     float* w = g.ws + ((uint64_t)blockIdx.y * g.m + row) * g.n + n;
     if (n + 8 <= g.n) {
       f8 o;

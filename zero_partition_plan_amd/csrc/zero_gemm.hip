@@ -133,18 +133,22 @@ hipError_t run_few(const GemmDev& d, hipStream_t s) {
   return hipGetLastError();
 }
 
-// What a tile of each shape takes, in us on MI355X: `fixed` besides its steps (start, epilogue), a
-// step (64 k) with the card almost empty and with `per_cu` tiles on every CU. Fitted to products
-// of 333 to 8192 rows; tiles of 128 x 128 and less win where there are few, as their fixed part
-// is shorter, tiles of 256 x 256 where there are many, as they read least.
+// What a tile of each shape takes, in us on MI355X: besides its steps (start and epilogue) with the
+// card almost empty and full, and a step (64 k) with the card almost empty and with `per_cu` tiles on
+// every CU. Fitted to products of 16 to 4096 rows, 768 to 50256 columns and k of 16 to 11008:
+// tiles of 128 x 128 and less win where there are few, as the part besides the steps is shorter
+// (333 x 2304 over k 768: 6.4 us against 20), tiles of 256 x 256 where there are many, as they read
+// least (4096 x 11008 over 4096: 281 us against 311), those of 192 where 256 leave CUs idle (2048 x 5120
+// over 5120: 87 us against 102).
 struct TileShape {
   uint32_t bm, bn, per_cu;
-  float fixed, alone, full;
+  float rest_alone, rest_full, alone, full;
 };
-constexpr TileShape kShapes[] = {{256, 256, 1, 7.0f, 1.0f, 1.45f},  {128, 256, 1, 6.5f, 0.58f, 0.92f},
-                                 {256, 128, 1, 6.5f, 0.62f, 0.94f}, {128, 128, 2, 5.4f, 0.43f, 0.87f},
-                                 {64, 256, 2, 5.5f, 0.43f, 0.95f},  {32, 256, 2, 4.2f, 0.41f, 0.81f},
-                                 {64, 64, 5, 3.4f, 0.27f, 1.0f}};
+constexpr TileShape kShapes[] = {{256, 256, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 5.8f, 5.8f, 0.59f, 0.84f},
+                                 {256, 128, 1, 5.9f, 8.0f, 0.60f, 0.84f},  {128, 128, 2, 5.1f, 5.1f, 0.38f, 0.77f},
+                                 {64, 256, 2, 5.2f, 5.2f, 0.44f, 0.90f},   {32, 256, 2, 3.9f, 3.9f, 0.42f, 0.70f},
+                                 {64, 64, 5, 3.1f, 3.1f, 0.27f, 0.84f},    {256, 192, 1, 8.4f, 12.0f, 0.74f, 1.00f},
+                                 {192, 256, 1, 7.4f, 7.4f, 0.78f, 1.05f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 constexpr uint32_t kCus = 256;
 
@@ -165,10 +169,12 @@ Plan plan(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t slots = kCus * t.per_cu;
     for (uint64_t sp = 1; sp <= 32 && (sp == 1 || steps / sp >= 2); ++sp) {
       const uint64_t per = (steps + sp - 1) / sp, splits = (steps + per - 1) / per;
-      const uint64_t all = tiles * splits, rounds = all / slots, rest = all % slots;
-      float time = (float)rounds * (t.fixed + (float)per * t.full);
-      if (rest)
-        time += t.fixed + (float)per * (t.alone + (t.full - t.alone) * (float)rest / (float)slots);
+      const uint64_t all = tiles * splits, rounds = all / slots, last = all % slots;
+      float time = (float)rounds * (t.rest_full + (float)per * t.full);
+      if (last) {
+        const float part = (float)last / (float)slots;
+        time += t.rest_alone + (float)per * (t.alone + (t.full - t.alone) * part);
+      }
       // the join's launch, and the partial sums written and read at some 4 TB/s
       if (splits > 1) time += 2.5f + (float)(m * n * splits) * 8.0f / 4e6f;
       if (time < best_t) {
@@ -202,7 +208,7 @@ hipError_t gemm(const GemmArgs& g, hipStream_t s) {
   const bool dir = direct(g.a, g.lda) && direct(g.b, g.ldb);
   const bool bf = g.dtype == ZERO_BF16;
   Plan p = plan(g.m, g.n, g.k);
-  if (!dir && p.shape == 0) p.shape = 1;  // the same splits, so the same workspace
+  if (!dir && (p.shape == 0 || p.shape == 7 || p.shape == 8)) p.shape = 1;  // the same splits and workspace
   GemmDev d{};
   d.a = g.a, d.b = g.b, d.bias = g.bias, d.res = g.res, d.pre = g.pre, d.out = g.out, d.ws = g.ws;
   d.lda = g.lda, d.ldb = g.ldb, d.ldr = g.ldr, d.ldp = g.ldp, d.ldo = g.ldo;

@@ -29,7 +29,7 @@ typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = kGemmStep;
-constexpr int kStages = 2;  // LDS stages
+constexpr int kStages = 2;  // LDS stages; 3 and 4 measured the same
 
 [[maybe_unused]] __device__ __forceinline__ f4 mfma(t8 a, t8 b, f4 c) {
 #if ZERO_GEMM_DT == 2
@@ -69,9 +69,9 @@ struct Tile {
   static constexpr int kElems = R * kStepK;
 
   static __device__ __forceinline__ int swz(int k) {
-    static_assert(R % 128 == 0 || R == 64 || R == 32, "whole granules, apart in 256 bytes");
+    static_assert(R % 128 == 0 || R % 128 == 64 || R == 32, "whole granules, apart in 256 bytes");
     const int half = k >> 3 & 1;
-    return R % 128 == 0 ? (k & 3) << 1 | half : R == 64 ? (k & 2) | half : half;
+    return R % 128 == 0 ? (k & 3) << 1 | half : R % 64 == 0 ? (k & 2) | half : half;
   }
 
   // (row, k) of the chunk that lies at place q of the tile
@@ -256,21 +256,20 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   const int part = DIRECT && k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
   const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
   Frags<S> f = {};
-  if (steps > 0) {
-    if (DIRECT) {
-      if (k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
-      ta.dma(ca.p, ca.bytes(k_left), lds, wave);
-      tb.dma(cb.p, cb.bytes(k_left), lds + S::kB, wave);
-    } else {
-      ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
-      tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
-      ta.put(lds, tid);
-      tb.put(lds + S::kB, tid);
-    }
+  if (DIRECT) {
+    if (k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
+    ta.dma(ca.p, ca.bytes(k_left), lds, wave);
+    tb.dma(cb.p, cb.bytes(k_left), lds + S::kB, wave);
+  } else {
+    ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
+    tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
+    ta.put(lds, tid);
+    tb.put(lds + S::kB, tid);
   }
-  auto body = [&](auto parity, bool last) {
-    constexpr int P = decltype(parity)::value;
+  auto body = [&](auto place, bool last) {
+    constexpr int P = decltype(place)::value, D = 1 - P;
     T *sa = lds + P * S::A::kElems, *sb = lds + S::kB + P * S::B::kElems;
+    T *da = lds + D * S::A::kElems, *db = lds + S::kB + D * S::B::kElems;
     ca.advance();
     cb.advance();
     k_left -= kStepK;
@@ -285,7 +284,6 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
       zero_partial<T, kBK, BN>(sb, k_last, tid, S::NT);
       __syncthreads();
     }
-    T *da = lds + (1 - P) * S::A::kElems, *db = lds + S::kB + (1 - P) * S::B::kElems;
     if (!DIRECT) {
       ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
       tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
@@ -324,9 +322,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     __builtin_amdgcn_wave_barrier();
     // two rows of a lane at a time: more in flight would spill the 256 x 256 tile's sums
     constexpr int kPer = 64 / kLanes, R = 2;
+    const uint32_t first = m0 + wm0 + i * 32, m_end = first + 32 < g.m ? first + 32 : g.m;
 #pragma unroll 1
-    for (int r0 = lane / kLanes; r0 < 32; r0 += R * kPer) {
-      const uint32_t m = m0 + wm0 + i * 32 + r0, n = n0 + wn0 + (lane % kLanes) * 8;
+    for (int r0 = lane / kLanes; r0 < (64 % kLanes && lane >= kPer * kLanes ? 0 : 32); r0 += R * kPer) {
+      const uint32_t m = first + r0, n = n0 + wn0 + (lane % kLanes) * 8;
       const float* at = stage + r0 * kRow + (lane % kLanes) * 8;
       float z[R][8];
 #pragma unroll
@@ -334,17 +333,17 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
         *reinterpret_cast<float4*>(&z[r][0]) = *reinterpret_cast<const float4*>(at + r * kPer * kRow);
         *reinterpret_cast<float4*>(&z[r][4]) = *reinterpret_cast<const float4*>(at + r * kPer * kRow + 4);
       }
-      if (m >= g.m || n >= g.n) continue;
+      if (m >= m_end || n >= g.n) continue;
       if (g.splits > 1) {
-        keep_rows<R>(g, z, m, kPer, n);
+        keep_rows<R>(g, z, m, kPer, m_end, n);
       } else if (n + 8 <= g.n) {
-        finish_rows<T, R>(g, z, m, kPer, n);
+        finish_rows<T, R>(g, z, m, kPer, m_end, n);
       } else {
 #pragma unroll 1
         for (int r = 0; r < R; ++r)
 #pragma unroll 1
           for (int j = 0; n + j < g.n; ++j)
-            if (m + r * kPer < g.m) finish_one<T>(g, at[r * kPer * kRow + j], m + r * kPer, n + j);
+            if (m + r * kPer < m_end) finish_one<T>(g, at[r * kPer * kRow + j], m + r * kPer, n + j);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -352,8 +351,6 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
 #endif
 }
 
-// The 256 x 256 tile takes direct loads only: with the operands held in registers on their way it
-// would spill.
 template <bool DIRECT, int BM, int BN, int WM, int WN>
 hipError_t launch(const GemmDev& g, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
@@ -382,8 +379,10 @@ hipError_t launch(const GemmDev& g, hipStream_t s) {
 #define ZERO_CAT(a, b, c, d) ZERO_CAT_(a, b, c, d)
 hipError_t ZERO_CAT(gemm_tiles_, ZERO_GEMM_DT, ZERO_GEMM_AK, ZERO_GEMM_BK)(const GemmDev& g, int shape,
                                                                            bool direct, hipStream_t s) {
-#define ZERO_SHAPE(id, ...) \
-  case id: return direct ? launch<true, __VA_ARGS__>(g, s) : launch<id == 0, __VA_ARGS__>(g, s);
+  // `held`: whether there is a kernel for operands that go through registers; the largest tiles would
+  // spill with them
+#define ZERO_SHAPE(id, held, ...) \
+  case id: return direct ? launch<true, __VA_ARGS__>(g, s) : launch<!held, __VA_ARGS__>(g, s);
   switch (shape) {
     ZERO_GEMM_SHAPES
     default: return hipErrorInvalidValue;
