@@ -1,5 +1,20 @@
 // Tile kernels of the matrix product, for one 16-bit type and one pair of operand orders (set by
 // ZERO_GEMM_DT, ZERO_GEMM_AK, ZERO_GEMM_BK when this file is compiled).
+//
+// out[i, j] = epilogue(sum_k A(i, k) B(j, k)), the sum in fp32 by the 16x16x32 matrix instruction. A
+// workgroup takes a tile of out and walks k in stages of 64, two stages in LDS: one is read into
+// fragments while the other is loaded, straight from memory to LDS (16 bytes a lane, bounds by the
+// buffer descriptor, so ragged edges read zeros). One barrier a stage; the fragments of the next 32
+// k are read behind the matrix instructions of these, across the barrier too. A k-contiguous operand is
+// read from LDS as it lies, a k-major one (dz and the weight in dz W, both operands of dz^T x) by the transposing
+// LDS read, so no operand is ever transposed in memory.
+//
+// What bounds it is power: on 8192^3 random bf16 the 256 x 256 tile reaches 1360 (x W^T), 1380 (dz W) and
+// 1440 TFLOP/s (dz^T x) at about 1.6 GHz, on zeros 1540 to 1710; hence the instruction with the
+// fewest trips of the sums through the matrix unit (the 32x32x16 one: 5 to 9% less), and two stages of
+// 64 k rather than more of 32 (a second barrier per 64 k: 10 to 20% less). 8 waves of 128 x 64 sums
+// each read LDS conflict-free at half its rate; 4 waves of 128 x 128 would read less but do not fit the registers.
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,7 +44,7 @@ typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = kGemmStep;
-constexpr int kStages = 2;  // LDS stages; 3 and 4 measured the same
+constexpr int kStages = 2;  // 3 and 4, where they fit, measured the same
 
 [[maybe_unused]] __device__ __forceinline__ f4 mfma(t8 a, t8 b, f4 c) {
 #if ZERO_GEMM_DT == 2
