@@ -225,7 +225,8 @@ __device__ __forceinline__ void add(const Args& a, MaxSum& r, float (&f)[N], uin
 }
 
 // NV: 16-byte vectors of the row that a thread of the step holds in registers; 0: reads it again.
-template <typename T, bool TAIL, int MODE, int NV, int NT>
+// STREAM: the gradient goes past the caches.
+template <typename T, bool TAIL, int MODE, int NV, int NT, bool STREAM>
 __global__ __launch_bounds__(NT) void k_distill(Args a) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   __shared__ MaxSum s_ms[NT / 64];
@@ -364,7 +365,8 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
       V y;
 #pragma unroll
       for (int j = 0; j < W; ++j) y[j] = (T)(fout * ex2(mul_s<T>(a, (float)x[j] - m)));
-      *reinterpret_cast<V*>(dz + (uint64_t)i * W) = y;
+      if constexpr (STREAM) __builtin_nontemporal_store(y, reinterpret_cast<V*>(dz + (uint64_t)i * W));
+      else *reinterpret_cast<V*>(dz + (uint64_t)i * W) = y;
     };
     if constexpr (NV > 0) {
 #pragma unroll
@@ -400,7 +402,17 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
 template <typename T, bool TAIL, int MODE, int NV, int NT>
 hipError_t launch_one(const Args& a, hipStream_t s) {
   const size_t lds = ((a.in.vocab + 127) / 128 * 4 + 3 * a.in.topk) * 4;
-  k_distill<T, TAIL, MODE, NV, NT><<<dim3((unsigned)a.in.rows), dim3(NT), lds, s>>>(a);
+  const dim3 grid((unsigned)a.in.rows), block(NT);
+  // A gradient of 128 MiB and more would push the logits out of the memory side cache, whether the
+  // forward or the head's product left them there (4096 x 32000 bf16 two calls 157 us past the caches,
+  // 174 through them); a smaller one stays for whoever reads it next (8192 x 4096 bf16 28 and 26 us).
+  if constexpr ((MODE & 2) != 0) {
+    if (a.in.rows * a.in.vocab * sizeof(T) >= (128ull << 20)) {
+      k_distill<T, TAIL, MODE, NV, NT, true><<<grid, block, lds, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  k_distill<T, TAIL, MODE, NV, NT, false><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
 }
 

@@ -91,6 +91,10 @@ __device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], 
                                             uint32_t m_end, uint32_t n) {
   typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
   typedef float f8 __attribute__((ext_vector_type(8), aligned(4)));
+  // A tile's results go past the caches: written back in turn they took from the operands' share of the
+  // memory side cache (2048 x 768 -> 50257 from cold operands 203 us, 249 without; a chain of 4096 x 4096
+  // and 11008 layers forward and backward, each reading the one before, 1 to 4% faster).
+  constexpr bool kStream = R > 1;
   const T* res = static_cast<const T*>(g.res) + m * g.ldr + n;
   T* pre = static_cast<T*>(g.pre) + m * g.ldp + n;
   float* out32 = static_cast<float*>(g.out) + m * g.ldo + n;
@@ -115,7 +119,9 @@ __device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], 
       v8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (T)z[r][j];
-      if (there(r)) *reinterpret_cast<v8*>(pre + (uint64_t)r * dm * g.ldp) = o;
+      if (!there(r)) continue;
+      if constexpr (kStream) __builtin_nontemporal_store(o, reinterpret_cast<v8*>(pre + (uint64_t)r * dm * g.ldp));
+      else *reinterpret_cast<v8*>(pre + (uint64_t)r * dm * g.ldp) = o;
     }
   }
   act_rt<R * 8>(&z[0][0], g.act);
@@ -140,7 +146,9 @@ __device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], 
       f8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = z[r][j];
-      if (there(r)) *reinterpret_cast<f8*>(out32 + (uint64_t)r * dm * g.ldo) = o;
+      if (!there(r)) continue;
+      if constexpr (kStream) __builtin_nontemporal_store(o, reinterpret_cast<f8*>(out32 + (uint64_t)r * dm * g.ldo));
+      else *reinterpret_cast<f8*>(out32 + (uint64_t)r * dm * g.ldo) = o;
     }
   } else {
     if (g.accumulate) {
@@ -157,7 +165,9 @@ __device__ __forceinline__ void finish_rows(const GemmDev& g, float (&z)[R][8], 
       v8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (T)z[r][j];
-      if (there(r)) *reinterpret_cast<v8*>(out16 + (uint64_t)r * dm * g.ldo) = o;
+      if (!there(r)) continue;
+      if constexpr (kStream) __builtin_nontemporal_store(o, reinterpret_cast<v8*>(out16 + (uint64_t)r * dm * g.ldo));
+      else *reinterpret_cast<v8*>(out16 + (uint64_t)r * dm * g.ldo) = o;
     }
   }
 }
