@@ -149,10 +149,10 @@ struct TileShape {
   uint32_t bm, bn, per_cu;
   float rest_alone, rest_full, alone, full;
 };
-constexpr TileShape kShapes[] = {{256, 256, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 5.8f, 5.8f, 0.59f, 0.84f},
-                                 {256, 128, 1, 5.9f, 8.0f, 0.60f, 0.84f},  {128, 128, 2, 5.1f, 5.1f, 0.38f, 0.77f},
-                                 {64, 256, 2, 5.2f, 5.2f, 0.44f, 0.90f},   {32, 256, 2, 3.9f, 3.9f, 0.42f, 0.70f},
-                                 {64, 64, 5, 3.1f, 3.1f, 0.27f, 0.84f},    {256, 192, 1, 8.4f, 12.0f, 0.74f, 1.00f},
+constexpr TileShape kShapes[] = {{256, 256, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 5.8f, 5.8f, 0.62f, 0.95f},
+                                 {256, 128, 1, 5.9f, 8.0f, 0.64f, 0.95f},  {128, 128, 2, 5.1f, 5.1f, 0.40f, 0.88f},
+                                 {64, 256, 2, 5.2f, 5.2f, 0.46f, 1.00f},   {32, 256, 2, 3.9f, 3.9f, 0.43f, 0.80f},
+                                 {64, 64, 5, 3.1f, 3.1f, 0.27f, 0.95f},    {256, 192, 1, 8.4f, 12.0f, 0.74f, 1.00f},
                                  {192, 256, 1, 7.4f, 10.0f, 0.78f, 1.05f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 constexpr uint32_t kCus = 256;
