@@ -70,7 +70,7 @@ SIZES = [(1, 1, 1), (1, 64, 64), (2, 8, 3), (7, 33, 5), (16, 128, 64), (17, 96, 
          (33, 256, 255), (64, 64, 64), (65, 72, 136), (127, 129, 128), (128, 640, 384), (200, 333, 77),
          (256, 256, 256), (257, 520, 263), (300, 2048, 40), (1000, 88, 1003), (512, 768, 512), (1030, 1024, 776)]
 # (element offset, padding of each row; "to 8": up to a multiple of 8 beyond the row)
-PLACES = [(0, 0), (8, 8), (1, 0), (3, 5), (8, "to 8")]
+PLACES = [(0, 0), (8, 8), (1, 0), (3, 5), (8, "to 8"), (2, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

@@ -192,7 +192,7 @@ Plan plan(uint64_t m, uint64_t n, uint64_t k) {
 }
 
 bool direct(const void* p, uint64_t ld) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && ld <= (1u << 22);
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0 && ld <= (1u << 22);
 }
 
 

@@ -59,8 +59,8 @@ struct Int {
   static constexpr int value = V;
 };
 
-// s_waitcnt for every load into LDS and every LDS access of this wave
-constexpr int kWaitAll = 0x0070;
+// s_waitcnt for every load into LDS and every LDS access of this wave, and for the LDS accesses alone
+[[maybe_unused]] constexpr int kWaitAll = 0x0070, kWaitLds = 0xc07f;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 
@@ -136,6 +136,17 @@ struct Tile {
   // element, and single elements at the edges.
   t8 held[kRounds];
   __device__ __forceinline__ void fetch(const T* base, uint64_t ld, uint32_t rows_left, int k_left, int tid) {
+    // whole steps, which is all but the last: plain loads (rows past the end repeat the last one)
+    if (k_left >= kStepK && (!KM || rows_left >= R)) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        int row, k;
+        chunk_at(r * NT + tid, row, k);
+        if (!KM) row = row < (int)rows_left ? row : (int)rows_left - 1;
+        held[r] = *reinterpret_cast<const t8u*>(base + (KM ? (uint64_t)k * ld + row : (uint64_t)row * ld + k));
+      }
+      return;
+    }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       int row, k;
@@ -281,18 +292,31 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     ta.put(lds, tid);
     tb.put(lds + S::kB, tid);
   }
-  auto body = [&](auto place, bool last) {
-    constexpr int P = decltype(place)::value, D = 1 - P;
-    T *sa = lds + P * S::A::kElems, *sb = lds + S::kB + P * S::B::kElems;
-    T *da = lds + D * S::A::kElems, *db = lds + S::kB + D * S::B::kElems;
+  // Held operands run two steps ahead: a step first puts what was asked for during the one before into
+  // the free stage, and asks for the next.
+  auto next = [&]() __attribute__((always_inline)) {
     ca.advance();
     cb.advance();
     k_left -= kStepK;
+  };
+  auto fetch = [&]() __attribute__((always_inline)) {
+    ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
+    tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
+  };
+  if (!DIRECT) {
+    next();
+    fetch();
+  }
+  auto body = [&](auto place, bool last) __attribute__((always_inline)) {
+    constexpr int P = decltype(place)::value, D = 1 - P;
+    T *sa = lds + P * S::A::kElems, *sb = lds + S::kB + P * S::B::kElems;
+    T *da = lds + D * S::A::kElems, *db = lds + S::kB + D * S::B::kElems;
+    if (DIRECT) next();
     const uint32_t abytes = ca.bytes(k_left), bbytes = cb.bytes(k_left);
     if (DIRECT && k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
     // what the next stage needs has landed, and this wave's reads of the stage that is to be loaded
     // over are done: the barrier makes both true of all waves
-    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    __builtin_amdgcn_s_waitcnt(DIRECT ? kWaitAll : kWaitLds);
     __syncthreads();
     if (part && last) {
       zero_partial<T, kAK, BM>(sa, k_last, tid, S::NT);
@@ -300,14 +324,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
       __syncthreads();
     }
     if (!DIRECT) {
-      ta.fetch(ca.p, g.lda, g.m - m0, k_left, tid);
-      tb.fetch(cb.p, g.ldb, g.n - n0, k_left, tid);
-    }
-    step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, f, acc, wm0, wn0, wave, lane);
-    if (!DIRECT) {
       ta.put(da, tid);
       tb.put(db, tid);
+      next();
+      fetch();
     }
+    step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, f, acc, wm0, wn0, wave, lane);
   };
   for (int s = 0; s < steps; s += 2) {
     body(Int<0>{}, s + 1 == steps);
