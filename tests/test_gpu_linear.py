@@ -136,6 +136,28 @@ def test_backward_whole_numbers(m, k, n, place, dtype, grad):
         p.check_canary(what)
 
 
+@pytest.mark.parametrize("m,k,n", [(4100, 4097, 4099), (4100, 4104, 4099), (4100, 4097, 4096), (9000, 771, 5003)])
+@pytest.mark.parametrize("off,pad", [(0, 0), (1, 1), (8, "to 8")])
+def test_large_odd_sizes(m, k, n, off, pad):
+    """Sizes at which rows off 16 bytes are copied before the products; whole numbers, exact in fp32."""
+    banner(f"linear large odd m={m} k={k} n={n} off={off} pad={pad}")
+    dt, g = torch.bfloat16, gen(m + k + n)
+    nan = float("nan")
+    x = Placed(m, k, dt, off, pad, nan).set(ints(g, m, k))
+    w = Placed(n, k, dt, off, 0, nan).set(ints(g, n, k))
+    dy = Placed(m, n, dt, off, pad, nan).set(ints(g, m, n))
+    y, dx, dw, db = Placed(m, n, dt, off, pad), Placed(m, k, dt, off, pad), Placed(n, k, torch.float32, off), Placed(1, n, torch.float32, off)
+    Z.zero_linear_forward(x.t, w.t, y.t, workspace=ws(m, k, n))
+    Z.zero_linear_backward(dy.t, x.t, w.t, dx=dx.t, dweight=dw.t, dbias=db.t[0], workspace=ws(m, k, n, True))
+    X, W, D = x.t.float().contiguous(), w.t.float().contiguous(), dy.t.float().contiguous()
+    same(y.t, X @ W.t(), "y")
+    same(dx.t, D @ W, "dx")
+    same(dw.t, D.t() @ X, "dweight")
+    same(db.t[0], D.sum(0), "dbias")
+    for p, what in ((y, "y"), (dx, "dx"), (dw, "dweight"), (db, "dbias")):
+        p.check_canary(what)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("kind", L.ACTS)
 @pytest.mark.parametrize("m,k,n", [(5, 64, 48), (70, 200, 131), (257, 512, 264)])
