@@ -11,9 +11,9 @@
 // Memory is the bound: the loss alone and the gradient alone read the row once, and the step keeps the
 // row in registers between the two, as far as it fits (a row of 131072 16-bit or 65536 fp32 logits);
 // longer rows are read twice, the second time mostly from cache. Measured, with what a large copy reaches
-// 5.1 TB/s: 8192 x 32000 bf16 loss and gradient 205 us (5.1 TB/s), 4096 x 50257 bf16 192 us (4.3, its rows lie off
+// 5.1 TB/s: 8192 x 32000 bf16 loss and gradient 210 us (5.0 TB/s), 4096 x 50257 bf16 192 us (4.3, its rows lie off
 // 16 bytes), 4096 x 32000 bf16 loss alone 46 us (5.7), 1024 x 50257 fp32 with a tail 114 us (3.6: rows of
-// 201 kB leave one or two to a CU, so loads, arithmetic and stores overlap less), one row of 50257 9.5 us, which is its chain
+// 201 kB leave one or two to a CU, so loads, arithmetic and stores overlap less), one row of 50257 9.1 us, which is its chain
 // of loads and reductions.
 #include <hip/hip_runtime.h>
 #include <math.h>

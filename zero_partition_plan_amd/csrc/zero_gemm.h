@@ -11,7 +11,7 @@ namespace zero {
 
 constexpr uint32_t kGemmStep = 64;  // k per LDS stage; splits of k are whole stages
 
-// Tile shapes: number, whether operands off 16 bytes may take it, rows, columns, waves along the rows,
+// Tile shapes: number, whether operands off 4 bytes may take it, rows, columns, waves along the rows,
 // waves along the columns.
 #define ZERO_GEMM_SHAPES               \
   ZERO_SHAPE(0, false, 256, 256, 2, 4) \
