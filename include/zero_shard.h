@@ -445,7 +445,7 @@ uint64_t zero_linear_workspace_bytes(uint64_t rows, uint64_t in_features, uint64
  * workspace must not overlap any array of the call. Column slices of one buffer do not overlap.
  * Errors: NULLs, a leading dimension below the columns, aliasing, an unknown act, an array off its
  * element size, a workspace that is missing, too small or off 16 bytes -> ZERO_E_INVAL; dtype
- * ZERO_F32 -> ZERO_E_UNSUPPORTED; a size above 2^31 - 1 or a byte count >= 2^63 ->
+ * ZERO_F32 -> ZERO_E_UNSUPPORTED; a size above 2^27 or a byte count >= 2^63 ->
  * ZERO_E_OVERFLOW. */
 zero_status zero_linear_forward(const zero_linear_shape* s, const void* x, uint64_t ldx,
                                 const void* weight, const void* bias, const void* residual,

@@ -249,3 +249,27 @@ def test_device_refusals():
         Z.zero_distill_step(s["logits"], s["idx"], s["top"], 0.0, loss, torch.empty(4, 50, device=DEV))
     with pytest.raises(TypeError):
         Z.zero_distill_step(s["logits"], s["idx"], s["top"], 1.0, loss, torch.empty(4, 50, device=DEV).half())
+
+
+@pytest.mark.parametrize("kind", ["step", "calls"])
+def test_more_rows_than_one_grid_dimension_holds(kind):
+    """2^24 rows of 256 threads are 2^32. One listed entry at T = 1 is the cross entropy of a label.
+    fp32 with 3 logits of at most 4: loss and gradient within a few dozen roundings of numbers up to 12."""
+    R, V = (1 << 24) + 5, 3
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    z = torch.rand(R, V, generator=g, device=DEV) * 8 - 4
+    idx = torch.randint(V, (R, 1), generator=g, device=DEV)
+    top = torch.zeros(R, 1, device=DEV)
+    loss, grad = torch.full((R,), -1.0, device=DEV), torch.full((R, V), -9.0, device=DEV)
+    if kind == "step":
+        Z.zero_distill_step(z, idx, top, 1.0, loss, grad)
+    else:
+        stats = torch.empty(R, 2, device=DEV)
+        Z.zero_distill_forward(z, idx, top, 1.0, loss, stats)
+        Z.zero_distill_backward(z, idx, top, 1.0, stats, grad)
+    lq = torch.log_softmax(z.double(), 1)
+    want = lq.exp().scatter_add(1, idx, torch.full((R, 1), -1.0, dtype=torch.double, device=DEV))
+    torch.cuda.synchronize()
+    assert float((loss.double() + lq.gather(1, idx)[:, 0]).abs().max()) <= 400 * U
+    assert float((grad.double() - want).abs().max()) <= 400 * U

@@ -321,3 +321,19 @@ def test_device_refusals():
         Z.zero_linear_forward(x[:1].expand(4, 8), w, y)                        # row stride 0
     with pytest.raises(TypeError):
         Z.zero_linear_backward(y, x, w, dweight=torch.zeros(4, 8, dtype=torch.float64, device=DEV))
+
+
+def test_more_small_tiles_than_a_grid_holds():
+    """A result of more than 2^35 elements (69 GB) over a short k, where small tiles would be fastest."""
+    m, k, n = 131077, 8, 262148
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB")
+    g = gen(9)
+    x, w = ints(g, m, k).bfloat16(), ints(g, n, k).bfloat16()
+    y = torch.empty(m, n, dtype=torch.bfloat16, device=DEV)
+    Z.zero_linear_forward(x, w, y, workspace=ws(m, k, n))
+    wt = w.float().t().contiguous()
+    for r in range(0, m, 8192):                    # whole numbers of at most 72: exact in bf16
+        assert torch.equal(y[r:r + 8192], (x[r:r + 8192].float() @ wt).bfloat16()), r
+    del y
+    torch.cuda.empty_cache()

@@ -173,3 +173,10 @@ def test_header_constants_match_binding():
     for name in ("NONE", "RELU", "GELU", "GELU_TANH", "SILU"):
         assert int(re.search(rf"ZERO_ACT_{name} = (\d)", text).group(1)) == getattr(Z, f"ZERO_ACT_{name}")
     assert ctypes.sizeof(Z.ZeroLinearShape) == 32 and ctypes.sizeof(Z.ZeroDistillIn) == 96
+
+
+def test_sizes_past_the_launch_limit_are_refused():
+    """A grid dimension holds fewer than 2^32 threads: the layer refuses what would need more."""
+    assert _fwd(_shape(rows=(1 << 27) + 1)) == OVERFLOW
+    assert _fwd(_shape(n=(1 << 27) + 1)) == OVERFLOW and _fwd(_shape(k=(1 << 27) + 1)) == OVERFLOW
+    assert Z.zero_linear_workspace_bytes((1 << 27) + 1, 8, 8) == 0

@@ -25,6 +25,7 @@ namespace zero {
 namespace {
 
 constexpr uint64_t kMaxSize = 0x7fffffffu;
+constexpr uint64_t kGridRows = 1u << 21;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -235,7 +236,8 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
   constexpr int W = Pack<T>::n;
   const zero_distill_in& in = a.in;
   const uint32_t K = (uint32_t)in.topk, vocab = (uint32_t)in.vocab;
-  const uint64_t row = blockIdx.x;
+  const uint64_t row = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= in.rows) return;
   const T* z = static_cast<const T*>(in.logits) + row * in.ld_logits;
   T* dz = static_cast<T*>(a.dlogits) + row * a.ldg;
   const int t = threadIdx.x, wave = t / 64;
@@ -402,7 +404,9 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
 template <typename T, bool TAIL, int MODE, int NV, int NT>
 hipError_t launch_one(const Args& a, hipStream_t s) {
   const size_t lds = ((a.in.vocab + 127) / 128 * 4 + 3 * a.in.topk) * 4;
-  const dim3 grid((unsigned)a.in.rows), block(NT);
+  // a row a block, over two dimensions, as one holds no more than 2^32 threads
+  const uint64_t wide = a.in.rows < kGridRows ? a.in.rows : kGridRows;
+  const dim3 grid((unsigned)wide, (unsigned)((a.in.rows + wide - 1) / wide)), block(NT);
   // A gradient of 128 MiB and more would push the logits out of the memory side cache, whether the
   // forward or the head's product left them there (4096 x 32000 bf16 two calls 157 us past the caches,
   // 174 through them); a smaller one stays for whoever reads it next (8192 x 4096 bf16 28 and 26 us).

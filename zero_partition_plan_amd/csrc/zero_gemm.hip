@@ -156,6 +156,7 @@ constexpr TileShape kShapes[] = {{256, 256, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128,
                                  {192, 256, 1, 7.4f, 10.0f, 0.78f, 1.05f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 constexpr uint32_t kCus = 256;
+constexpr uint64_t kMaxTiles = 1u << 23;  // of at most 512 threads: a grid dimension holds 2^32
 
 struct Plan {
   int shape;
@@ -222,9 +223,14 @@ hipError_t gemm(const GemmArgs& g, hipStream_t s) {
   const bool dir = direct(g.a, g.lda) && direct(g.b, g.ldb);
   Plan p = plan(g.m, g.n, g.k);
   if (!dir && (p.shape == 0 || p.shape == 7 || p.shape == 8)) p.shape = 1;  // the same splits and workspace
-  const uint64_t tiles_m = (g.m + (uint64_t)kShapes[p.shape].bm - 1) / kShapes[p.shape].bm;
-  const uint64_t tiles_n = (g.n + (uint64_t)kShapes[p.shape].bn - 1) / kShapes[p.shape].bn;
-  if (tiles_m * tiles_n > 0x7fffffffu) return hipErrorInvalidConfiguration;
+  uint64_t tiles_m, tiles_n;
+  for (int again = 0;; ++again) {
+    tiles_m = (g.m + (uint64_t)kShapes[p.shape].bm - 1) / kShapes[p.shape].bm;
+    tiles_n = (g.n + (uint64_t)kShapes[p.shape].bn - 1) / kShapes[p.shape].bn;
+    if (tiles_m * tiles_n < kMaxTiles) break;
+    if (again) return hipErrorInvalidConfiguration;
+    p.shape = 1;  // small tiles of a result of 2^35 elements and more: larger ones
+  }
   d.tiles_m = (uint32_t)tiles_m, d.tiles_n = (uint32_t)tiles_n;
   d.splits = p.splits, d.k_split = p.k_split;
   hipError_t e;

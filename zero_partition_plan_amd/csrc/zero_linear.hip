@@ -11,7 +11,7 @@
 namespace zero {
 namespace {
 
-constexpr uint64_t kMaxSize = 0x7fffffffu;
+constexpr uint64_t kMaxSize = 1u << 27;  // keeps every grid below 2^32 threads a dimension
 
 // dz = round16(dy * act'(pre)), 8 columns a thread, and the bias gradient's partial sums of the
 // stored dz: a block takes 256 columns and `chunk` rows, its 8 threads on a column every eighth row,
@@ -263,7 +263,7 @@ zero_status check_shape(const char* fn, const zero_linear_shape* s) {
   if (s->act < ZERO_ACT_NONE || s->act > ZERO_ACT_SILU)
     return fail(ZERO_E_INVAL, "%s: unknown activation %d", fn, s->act);
   if (s->rows > kMaxSize || s->in_features > kMaxSize || s->out_features > kMaxSize)
-    return fail(ZERO_E_OVERFLOW, "%s: a size above 2^31 - 1", fn);
+    return fail(ZERO_E_OVERFLOW, "%s: a size above 2^27", fn);
   return ZERO_OK;
 }
 
