@@ -337,3 +337,17 @@ def test_more_small_tiles_than_a_grid_holds():
         assert torch.equal(y[r:r + 8192], (x[r:r + 8192].float() @ wt).bfloat16()), r
     del y
     torch.cuda.empty_cache()
+
+
+# Few tiles and a long k: a tile's steps are shared by groups of waves, and by splits whose last has one,
+# two or three steps, so that a group has none, or the k ends inside a chunk of one group
+SHARED = [(200, 200, 2319), (200, 2319, 200), (200, 300, 1582), (200, 1582, 300), (1582, 300, 200), (333, 256, 2404),
+          (333, 2404, 256), (2404, 256, 333), (70, 523, 200), (333, 767, 2303)]
+
+
+@pytest.mark.parametrize("dtype,grad", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("place", [(0, 0), (1, 0), (3, 5), (8, "to 8")])
+@pytest.mark.parametrize("m,k,n", SHARED)
+def test_k_shared_by_groups_and_splits(m, k, n, place, dtype, grad):
+    test_forward_whole_numbers(m, k, n, place, dtype)
+    test_backward_whole_numbers(m, k, n, place, dtype, grad)

@@ -144,16 +144,19 @@ hipError_t run_few(const GemmDev& d, hipStream_t s) {
 // tiles of 128 x 128 and less win where there are few, as the part besides the steps is shorter
 // (333 x 2304 over k 768: 6.4 us against 20), tiles of 256 x 256 where there are many, as they read
 // least (4096 x 11008 over 4096: 281 us against 311), those of 192 where 256 leave CUs idle (2048 x 5120
-// over 5120: 87 us against 102).
+// over 5120: 87 us against 102), two groups of waves on a tile where few tiles walk a long k (1001 x 768
+// over 2304: 15.0 us against 20.6; four groups a tile gain less than 1% more over all). Measured on operands that
+// another kernel has just written: a step of few tiles takes up to twice as long there as on warm ones.
+// `groups` share a tile's steps, so a step counts once for all of them.
 struct TileShape {
-  uint32_t bm, bn, per_cu;
+  uint32_t bm, bn, per_cu, groups;
   float rest_alone, rest_full, alone, full;
 };
-constexpr TileShape kShapes[] = {{256, 256, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 5.8f, 5.8f, 0.62f, 0.95f},
-                                 {256, 128, 1, 5.9f, 8.0f, 0.64f, 0.95f},  {128, 128, 2, 5.1f, 5.1f, 0.40f, 0.88f},
-                                 {64, 256, 2, 5.2f, 5.2f, 0.46f, 1.00f},   {32, 256, 2, 3.9f, 3.9f, 0.43f, 0.80f},
-                                 {64, 64, 5, 3.1f, 3.1f, 0.27f, 0.95f},    {256, 192, 1, 8.4f, 12.0f, 0.74f, 1.00f},
-                                 {192, 256, 1, 7.4f, 10.0f, 0.78f, 1.05f}};
+constexpr TileShape kShapes[] = {{256, 256, 1, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 1, 5.8f, 5.8f, 0.62f, 0.95f},
+                                 {256, 128, 1, 1, 5.9f, 8.0f, 0.64f, 0.95f},  {128, 128, 2, 1, 5.1f, 5.1f, 0.40f, 0.88f},
+                                 {64, 256, 2, 1, 5.2f, 5.2f, 0.46f, 1.00f},   {32, 256, 2, 1, 3.9f, 3.9f, 0.43f, 0.80f},
+                                 {64, 64, 5, 1, 3.5f, 3.4f, 0.28f, 0.88f},    {256, 192, 1, 1, 8.4f, 12.0f, 0.74f, 1.00f},
+                                 {192, 256, 1, 1, 7.4f, 10.0f, 0.78f, 1.05f},  {64, 64, 2, 2, 3.7f, 3.8f, 0.40f, 0.98f}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 constexpr uint32_t kCus = 256;
 constexpr uint64_t kMaxTiles = 1u << 23;  // of at most 512 threads: a grid dimension holds 2^32
@@ -177,12 +180,13 @@ Plan plan(uint64_t m, uint64_t n, uint64_t k) {
     const float slots = (float)(kCus * t.per_cu);
     for (const uint32_t sp : kSplits) {
       if (sp > 1 && (steps / sp < 2 || (float)tiles * (float)sp > 4.0f * slots)) break;
-      const uint32_t per = (steps + sp - 1) / sp, splits = (steps + per - 1) / per;
+      const uint32_t turns = (steps + sp * t.groups - 1) / (sp * t.groups);  // steps of a group
+      const uint32_t per = turns * t.groups, splits = (steps + per - 1) / per;
       const float loads = (float)tiles * (float)splits / slots, rounds = floorf(loads), part = loads - rounds;
-      float time = rounds * (t.rest_full + (float)per * t.full);
-      if (part > 0.0f) time += t.rest_alone + (float)per * (t.alone + (t.full - t.alone) * part);
+      float time = rounds * (t.rest_full + (float)turns * t.full);
+      if (part > 0.0f) time += t.rest_alone + (float)turns * (t.alone + (t.full - t.alone) * part);
       // the join's launch, and the partial sums written and read at some 4 TB/s
-      if (splits > 1) time += 2.5f + (float)m * (float)n * (float)splits * 8.0f / 4e6f;
+      if (splits > 1) time += 3.0f + (float)m * (float)n * (float)splits * 8.0f / 4e6f;
       if (time < best_t) {
         best_t = time;
         best = Plan{i, splits, per * kGemmStep};

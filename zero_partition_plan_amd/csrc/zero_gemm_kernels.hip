@@ -253,12 +253,15 @@ __device__ __forceinline__ void step(const T* __restrict__ sa, const T* __restri
   }
 }
 
-template <typename S, bool DIRECT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
+// G groups of waves take the k steps of a tile between them, each with stages of its own, and are
+// joined through LDS in their order: where there are few tiles, the time is the chain of their steps.
+template <typename S, bool DIRECT, int BM, int BN, int WM, int WN, int G>
+__global__ __launch_bounds__(WM* WN * 64 * G, 2) void k_gemm(GemmDev g) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host's pass has no use for the body
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  T* lds = reinterpret_cast<T*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int group = G == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / S::NT);
+  T* lds = reinterpret_cast<T*>(smem) + group * S::kElems;
+  const int tid = G == 1 ? threadIdx.x : threadIdx.x % S::NT, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   uint32_t mt, nt;
   tile_of(g, blockIdx.x, mt, nt);
@@ -273,15 +276,21 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     ta.init(g.lda, tid);
     tb.init(g.ldb, tid);
   }
-  Cursor<T, kAK, BM> ca(g.a, g.lda, m0, g.m, k_begin);
-  Cursor<T, kBK, BN> cb(g.b, g.ldb, n0, g.n, k_begin);
+  // steps of the workgroup, and of each of its groups: a split that is not the last has a multiple of G, and
+  // what lies past the last one's end reads zeros
+  const int all = (int)((k_end - k_begin + kStepK - 1) / kStepK);
+  const int steps = (all + G - 1) / G;
+  const uint32_t k_first = k_begin + (uint32_t)(group * steps) * kStepK;
+  Cursor<T, kAK, BM> ca(g.a, g.lda, m0, g.m, k_first);
+  Cursor<T, kBK, BN> cb(g.b, g.ldb, n0, g.n, k_first);
 
   f4 acc[S::TM][S::TN] = {};
-  const int steps = (int)((k_end - k_begin + kStepK - 1) / kStepK);
-  int k_left = (int)(g.k - k_begin);
+  int k_left = (int)g.k - (int)k_first;
   // k's last, partial chunk of a k-contiguous row comes with what lies behind the row
   const int part = DIRECT && k_end == g.k && (!kAK || !kBK) ? (int)(g.k & 7) : 0;
-  const int k_last = (int)(k_end - k_begin) - (steps - 1) * kStepK;
+  const int k_last = (int)(k_end - k_begin) - (all - 1) * kStepK;
+  // the group and the step of that chunk
+  const int g_last = G == 1 || !all ? 0 : (all - 1) / steps, s_last = all - 1 - g_last * steps;
   Frags<S> f = {};
   if (DIRECT) {
     if (k_left < kStepK) ta.clip(k_left), tb.clip(k_left);
@@ -320,8 +329,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     __builtin_amdgcn_s_waitcnt(DIRECT ? kWaitAll : kWaitLds);
     __syncthreads();
     if (part && last) {
-      zero_partial<T, kAK, BM>(sa, k_last, tid, S::NT);
-      zero_partial<T, kBK, BN>(sb, k_last, tid, S::NT);
+      if (G == 1 || group == g_last) {
+        zero_partial<T, kAK, BM>(sa, k_last, tid, S::NT);
+        zero_partial<T, kBK, BN>(sb, k_last, tid, S::NT);
+      }
       __syncthreads();
     }
     if (!DIRECT) {
@@ -333,8 +344,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
     step<S, DIRECT>(sa, sb, da, db, ta, tb, ca.p, abytes, cb.p, bbytes, f, acc, wm0, wn0, wave, lane);
   };
   for (int s = 0; s < steps; s += 2) {
-    body(Int<0>{}, s + 1 == steps);
-    if (s + 1 < steps) body(Int<1>{}, s + 2 == steps);
+    body(Int<0>{}, s == s_last);
+    if (s + 1 < steps) body(Int<1>{}, s + 1 == s_last);
   }
 #pragma unroll
   for (int i = 0; i < S::TM; ++i)
@@ -347,7 +358,30 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
   // code for all (it would be the larger part of the kernel, fetched cold by every launch).
   constexpr int kRow = S::TN * 16 + 4;
   constexpr int kLanes = S::TN * 16 / 8;  // lanes on a row
-  float* stage = reinterpret_cast<float*>(smem) + wave * (32 * kRow);
+  float* stage = reinterpret_cast<float*>(smem) + (group * (WM * WN) + wave) * (32 * kRow);
+  if constexpr (G > 1) {
+    static_assert(S::TM == 2 && 64 / kLanes >= 32 / G, "one turn");
+#pragma unroll
+    for (int c = 0; c < S::TM; ++c)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j)
+        *reinterpret_cast<f4*>(stage + (c * 16 + (lane & 15)) * kRow + j * 16 + (lane >> 4) * 4) = acc[c][j];
+    __syncthreads();
+    // each group finishes its share of the rows
+    const int r = group * (32 / G) + lane / kLanes, col = (lane % kLanes) * 8;
+    const uint32_t m = m0 + wm0 + r, n = n0 + wn0 + col;
+    if (lane / kLanes < 32 / G && m < g.m && n < g.n) {
+      const float* at = reinterpret_cast<const float*>(smem) + wave * (32 * kRow) + r * kRow + col;
+      float z[1][8] = {};
+#pragma unroll
+      for (int h = 0; h < G; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[0][j] += at[h * (WM * WN * 32 * kRow) + j];
+      if (g.splits > 1) keep_rows<1>(g, z, m, 1, g.m, n);
+      else finish_row<T>(g, z, m, n);
+    }
+    return;
+  }
 #pragma unroll 1
   for (int i = 0; i < S::TM / 2; ++i) {
 #pragma unroll
@@ -389,12 +423,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm(GemmDev g) {
 #endif
 }
 
-template <bool DIRECT, int BM, int BN, int WM, int WN>
+template <bool DIRECT, int BM, int BN, int WM, int WN, int G>
 hipError_t launch(const GemmDev& g, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
   constexpr int epi = WM * WN * 32 * (S::TN * 16 + 4) * 4;
-  constexpr int lds = S::kElems * 2 > epi ? S::kElems * 2 : epi;
-  auto fn = k_gemm<S, DIRECT, BM, BN, WM, WN>;
+  constexpr int lds = G * (S::kElems * 2 > epi ? S::kElems * 2 : epi);
+  auto fn = k_gemm<S, DIRECT, BM, BN, WM, WN, G>;
   if (lds > 64 * 1024) {
     static std::atomic<uint64_t> allowed{0};  // one bit a device
     int dev = 0;
@@ -407,7 +441,7 @@ hipError_t launch(const GemmDev& g, hipStream_t s) {
       allowed.fetch_or(bit, std::memory_order_relaxed);
     }
   }
-  fn<<<dim3(g.tiles_m * g.tiles_n, g.splits), dim3(S::NT), lds, s>>>(g);
+  fn<<<dim3(g.tiles_m * g.tiles_n, g.splits), dim3(S::NT * G), lds, s>>>(g);
   return hipGetLastError();
 }
 
