@@ -1,6 +1,6 @@
 """A small ZeRO-3 training step made of the library's calls alone: gather, a two-layer MLP block on a
-residual stream, a head, the distillation loss, the backward into replica rows. Used by the GPU tests
-and the smoke check."""
+residual stream, a head, the distillation loss, the backward into replica rows. Used by the GPU
+tests of the operators together."""
 
 import torch
 

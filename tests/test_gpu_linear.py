@@ -351,3 +351,20 @@ SHARED = [(200, 200, 2319), (200, 2319, 200), (200, 300, 1582), (200, 1582, 300)
 def test_k_shared_by_groups_and_splits(m, k, n, place, dtype, grad):
     test_forward_whole_numbers(m, k, n, place, dtype)
     test_backward_whole_numbers(m, k, n, place, dtype, grad)
+
+
+@pytest.mark.parametrize("dtype,grad", [("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("rows", [1, 2, 8, 31, 32, 33, 64, 190, 200, 800])
+def test_bias_gradient_of_any_chunks(rows, dtype, grad):
+    """The bias gradient alone, written and added to, for rows of one chunk, of a few and of many."""
+    n, dt, g = 523, DT[dtype], gen(rows)
+    dy = Placed(rows, n, dt, 1, 3, fill=float("nan")).set(ints(g, rows, n))
+    x, w = torch.zeros(rows, 8, dtype=dt, device=DEV), torch.zeros(n, 8, dtype=dt, device=DEV)
+    db = Placed(1, n, DT.get(grad, torch.float32), 1)
+    want = dy.t.double().sum(0, keepdim=True)       # at most 2400: exact in fp32
+    Z.zero_linear_backward(dy.t, x, w, dbias=db.t[0], workspace=ws(rows, 8, n, True))
+    same(db.t, want, "dbias")
+    before = db.t.double().clone()
+    Z.zero_linear_backward(dy.t, x, w, dbias=db.t[0], accumulate=True, workspace=ws(rows, 8, n, True))
+    same(db.t, before + want, "dbias added to")
+    db.check_canary("dbias")

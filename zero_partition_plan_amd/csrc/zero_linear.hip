@@ -23,7 +23,8 @@ constexpr int kColsPerBlock = 256, kRowLanes = 8;
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void k_dz(const T* dy, uint64_t lddy, const T* pre, uint64_t ldp,
                                             T* dz, uint64_t lddz, uint32_t rows, uint32_t cols,
-                                            uint32_t chunk, float* sums) {
+                                            uint32_t chunk, float* sums, void* db, int db_f32,
+                                            int accumulate) {
   typedef T v8 __attribute__((ext_vector_type(8), aligned(2)));
   __shared__ float part[kRowLanes][kColsPerBlock + 4];
   const int cl = threadIdx.x % 32, rl = threadIdx.x / 32;
@@ -57,7 +58,7 @@ __global__ __launch_bounds__(256) void k_dz(const T* dy, uint64_t lddy, const T*
           s[j] += (float)d;
         }
   }
-  if (!sums) return;
+  if (!sums && !db) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) part[rl][cl * 8 + j] = s[j];
   __syncthreads();
@@ -66,7 +67,15 @@ __global__ __launch_bounds__(256) void k_dz(const T* dy, uint64_t lddy, const T*
   float v = 0.0f;
 #pragma unroll
   for (int l = 0; l < kRowLanes; ++l) v += part[l][threadIdx.x];
-  sums[(uint64_t)blockIdx.y * cols + col] = v;
+  if (sums) {
+    sums[(uint64_t)blockIdx.y * cols + col] = v;
+  } else if (db_f32) {  // the only chunk
+    float* o = static_cast<float*>(db) + col;
+    *o = accumulate ? v + *o : v;
+  } else {
+    T* o = static_cast<T*>(db) + col;
+    *o = (T)(accumulate ? v + (float)*o : v);
+  }
 }
 
 // dbias from the chunks' sums: 4 threads on a column, every fourth chunk each.
@@ -91,7 +100,11 @@ __global__ __launch_bounds__(256) void k_db(const float* sums, uint32_t chunks, 
 // Row chunks of the pass: enough blocks to fill the card several times, 32 rows a chunk at least where
 // there are 24 chunks of that (1000 x 2304 with the join 7.7 us, 9.3 with 8 rows), 8 rows below (333 x 2304 6.3
 // us against 7.2, 128 x 4096 5.2 against 6.4), and at most 128 chunks, which the join still reads in a few microseconds.
+// A single chunk needs no join: up to 32 rows the join's launch costs more than the chunks save (16 x 2304 3.5
+// us in one chunk, 4.9 in two and the join; 64 x 768 6.0 and 5.0).
+constexpr uint64_t kOneChunk = 32;
 uint32_t dz_chunks(uint64_t rows, uint64_t cols) {
+  if (rows <= kOneChunk) return 1;
   const uint64_t groups = (cols + kColsPerBlock - 1) / kColsPerBlock;
   const uint64_t eighths = (rows + 7) / 8 < 24 ? (rows + 7) / 8 : 24;
   uint64_t n = (rows + 31) / 32 > eighths ? (rows + 31) / 32 : eighths;
@@ -102,14 +115,15 @@ uint32_t dz_chunks(uint64_t rows, uint64_t cols) {
 
 template <typename T>
 hipError_t run_dz(int act, const void* dy, uint64_t lddy, const void* pre, uint64_t ldp, void* dz,
-                  uint64_t lddz, uint64_t rows, uint64_t cols, float* sums, hipStream_t s) {
+                  uint64_t lddz, uint64_t rows, uint64_t cols, float* sums, void* db, int db_f32, int accumulate,
+                  hipStream_t s) {
   const uint32_t chunks = dz_chunks(rows, cols);
   const uint32_t chunk = (uint32_t)((rows + chunks - 1) / chunks);
   const dim3 grid((unsigned)((cols + kColsPerBlock - 1) / kColsPerBlock), chunks);
 #define ZERO_DZ(A)                                                                             \
   k_dz<T, A><<<grid, dim3(256), 0, s>>>(static_cast<const T*>(dy), lddy,                       \
                                         static_cast<const T*>(pre), ldp, static_cast<T*>(dz), \
-                                        lddz, (uint32_t)rows, (uint32_t)cols, chunk, sums)
+                                        lddz, (uint32_t)rows, (uint32_t)cols, chunk, sums, db, db_f32, accumulate)
   switch (act) {
     case ZERO_ACT_NONE: ZERO_DZ(ZERO_ACT_NONE); break;
     case ZERO_ACT_RELU: ZERO_DZ(ZERO_ACT_RELU); break;
@@ -392,13 +406,16 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
   // the bias gradient's sums are joined before the products use the workspace for theirs
   float* ws = static_cast<float*>(workspace);
   const bool db_wanted = dbias && N && !(M == 0 && accumulate);
+  const bool one = dz_chunks(M, N) == 1;
   if ((has_act && M && N) || db_wanted) {
-    float* sums = db_wanted ? ws : nullptr;
-    e = bf ? run_dz<__bf16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, strm)
-           : run_dz<_Float16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, strm);
+    float* sums = db_wanted && !one ? ws : nullptr;
+    void* db = db_wanted && one ? dbias : nullptr;
+    const int f32 = grad_dtype == ZERO_F32;
+    e = bf ? run_dz<__bf16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, db, f32, accumulate, strm)
+           : run_dz<_Float16>(s->act, dy, m[0].ld, pre, m[3].ld, dz, m[4].ld, M, N, sums, db, f32, accumulate, strm);
   }
   if (has_act) d = dz, ldd = m[4].ld;
-  if (e == hipSuccess && db_wanted) {
+  if (e == hipSuccess && db_wanted && !one) {
     if (grad_dtype == ZERO_F32) e = run_db<float>(ws, M, N, dbias, accumulate, strm);
     else if (bf) e = run_db<__bf16>(ws, M, N, dbias, accumulate, strm);
     else e = run_db<_Float16>(ws, M, N, dbias, accumulate, strm);
