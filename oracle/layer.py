@@ -15,7 +15,16 @@ import numpy as np
 
 ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 _C, _A = math.sqrt(2.0 / math.pi), 0.044715
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+def _sigmoid(z):
+    with np.errstate(over="ignore"):                     # exp past fp64: 0
+        return 1.0 / (1.0 + np.exp(-z))
+
+
+# The gates are written without 1 + erf and 1 + tanh, whose digits cancel for negative z:
+# (1 + erf u)/2 = erfc(-u)/2 and (1 + tanh u)/2 = sigmoid(2u).
 
 
 def act(z: np.ndarray, kind: str) -> np.ndarray:
@@ -23,11 +32,11 @@ def act(z: np.ndarray, kind: str) -> np.ndarray:
     if kind == "relu":
         return np.maximum(z, 0.0)
     if kind == "gelu":
-        return z * (1.0 + _erf(z / math.sqrt(2.0))) / 2.0
+        return z * _erfc(-z / math.sqrt(2.0)) / 2.0
     if kind == "gelu_tanh":
-        return z * (1.0 + np.tanh(_C * (z + _A * z ** 3))) / 2.0
+        return z * _sigmoid(2.0 * _C * (z + _A * z ** 3))
     if kind == "silu":
-        return z / (1.0 + np.exp(-z))
+        return z * _sigmoid(z)
     return z
 
 
@@ -36,13 +45,12 @@ def act_slope(z: np.ndarray, kind: str) -> np.ndarray:
     if kind == "relu":
         return (z > 0).astype(np.float64)
     if kind == "gelu":
-        return (1.0 + _erf(z / math.sqrt(2.0))) / 2.0 + z * np.exp(-z * z / 2.0) / math.sqrt(2.0 * math.pi)
+        return _erfc(-z / math.sqrt(2.0)) / 2.0 + z * np.exp(-z * z / 2.0) / math.sqrt(2.0 * math.pi)
     if kind == "gelu_tanh":
-        t = np.tanh(_C * (z + _A * z ** 3))
-        return (1.0 + t) / 2.0 + z * (1.0 - t * t) / 2.0 * _C * (1.0 + 3.0 * _A * z * z)
+        u = 2.0 * _C * (z + _A * z ** 3)
+        return _sigmoid(u) * (1.0 + z * _sigmoid(-u) * 2.0 * _C * (1.0 + 3.0 * _A * z * z))
     if kind == "silu":
-        s = 1.0 / (1.0 + np.exp(-z))
-        return s * (1.0 + z * (1.0 - s))
+        return _sigmoid(z) * (1.0 + z * _sigmoid(-z))
     return np.ones_like(z)
 
 

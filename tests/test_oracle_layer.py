@@ -115,3 +115,23 @@ def test_rows_without_teacher_or_weight_are_zero():
     z[0, 3] = np.nan                                    # not read
     loss, grad = L.distill(z, idx, top, 1.0, None, w)
     assert (loss[:3] == 0).all() and (grad[:3] == 0).all() and (loss[3:] > 0).all()
+
+
+@pytest.mark.parametrize("kind", [k for k in L.ACTS if k != "none"])
+def test_activations_keep_their_digits_far_out(kind):
+    """Relative accuracy where a gate is small: scipy's normal distribution and logistic function, and the
+    slopes by the formula in their terms (an exponential of e is off by |e| roundings, at most 300 here)."""
+    from scipy import special
+    z = np.concatenate([np.linspace(-12, 12, 481), [-30.0, 30.0]]) + 1e-3
+    c, a = np.sqrt(2 / np.pi), 0.044715
+    u = 2 * c * (z + a * z ** 3)
+    phi = np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    y, first, second = {
+        "relu": (np.maximum(z, 0), (z > 0) * 1.0, 0 * z),
+        "gelu": (z * special.ndtr(z), special.ndtr(z), z * phi),
+        "gelu_tanh": (z * special.expit(u), special.expit(u),
+                      z * special.expit(u) * special.expit(-u) * 2 * c * (1 + 3 * a * z * z)),
+        "silu": (z * special.expit(z), special.expit(z), z * special.expit(z) * special.expit(-z)),
+    }[kind]
+    assert (np.abs(L.act(z, kind) - y) <= 1e-12 * np.abs(y)).all()
+    assert (np.abs(L.act_slope(z, kind) - (first + second)) <= 1e-12 * (first + np.abs(second))).all()

@@ -1,6 +1,8 @@
-// The linear layer's activations on the device, and 16-bit conversions. fp32 arithmetic; the results
-// are rounded to 16 bits by the caller, so the hardware's exp2 and reciprocal (about one unit in the last
-// fp32 place each) are far below what is kept.
+// The linear layer's activations on the device. fp32 arithmetic; the results are rounded to 16 bits by the
+// caller, so the hardware's exp2 and reciprocal (about one unit in the last fp32 place each) are far below what
+// is kept. Gates are formed so that they keep that accuracy where they are small: (1 + erf u)/2 by the
+// upper tail of the normal distribution (the sum has lost every digit at z = -5.75, where the result is still a bf16
+// of -2.6e-8), (1 + tanh u)/2 as the sigmoid of 2u.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,10 +21,34 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
 
+// The normal distribution's (1 + erf(z/sqrt 2))/2, and exp(-z^2/2). The tail beyond a = |z|
+// times exp(a^2/2) falls smoothly from 1/2 and as 1/a far out: a polynomial in t = 1/(1 + 0.305 a) without constant term,
+// its coefficients fitted for the least relative error on [0, 14] (9.4e-8; past 13.2 exp2 gives 0). One reciprocal, one
+// exp2 and no branch: 4096 x 4096 -> 11008 with gelu 328 us, 368 us with the math library's erfc, and 341 us with its
+// erf, which cancels.
+struct Normal {
+  float cdf, e;
+};
+__device__ __forceinline__ Normal normal(float z) {
+  const float a = __builtin_fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.305f, a, 1.0f));
+  const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * (z * z));
+  float p = 0.0366991907f;
+  p = __builtin_fmaf(p, t, -0.1529883f);
+  p = __builtin_fmaf(p, t, 0.185716867f);
+  p = __builtin_fmaf(p, t, -0.0379767939f);
+  p = __builtin_fmaf(p, t, 0.121021658f);
+  p = __builtin_fmaf(p, t, 0.103420876f);
+  p = __builtin_fmaf(p, t, 0.122466817f);
+  p = __builtin_fmaf(p, t, 0.121639736f);
+  const float q = p * t * e;
+  return Normal{z < 0.0f ? q : 1.0f - q, e};
+}
+
 template <int ACT>
 __device__ __forceinline__ float act(float z) {
   if constexpr (ACT == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z;  // keeps a NaN
-  if constexpr (ACT == ZERO_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+  if constexpr (ACT == ZERO_ACT_GELU) return z * normal(z).cdf;
   // (1 + tanh u)/2 = sigmoid(2u)
   if constexpr (ACT == ZERO_ACT_GELU_TANH)
     return z * sigmoid(2.0f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z));
@@ -34,10 +60,8 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == ZERO_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752440f));
-    // density exp(-z^2/2)/sqrt(2 pi)
-    return __builtin_fmaf(z * 0.39894228040143267794f,
-                          __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z), cdf);
+    const Normal n = normal(z);
+    return __builtin_fmaf(z * 0.39894228040143267794f, n.e, n.cdf);  // density exp(-z^2/2)/sqrt(2 pi)
   }
   if constexpr (ACT == ZERO_ACT_GELU_TANH) {
     const float z2 = z * z;
