@@ -455,9 +455,10 @@ zero_status zero_linear_forward(const zero_linear_shape* s, const void* x, uint6
 /* The gradients of zero_linear_forward from dy = dL/dy [rows, out]:
  *   dz = round16(dy * act'(pre))   (dz = dy itself, unwritten, for ZERO_ACT_NONE)
  *   dx = round16(dz W);  dweight = dz^T x;  dbias = sum over rows of dz
- * with the sums fp32 in a fixed order; the residual's gradient is dy. With an activation, pre and
- * dz [rows, out] are required (without one both are ignored). dx [rows, in], dweight [out, in]
- * contiguous and dbias [out]: any subset, at least one of the three or, with an activation, none.
+ * with the sums fp32 in a fixed order; the residual's gradient is dy. act' at an infinite pre (an
+ * overflow of its type) is its limit, 0 or 1. With an activation, pre and dz [rows, out] are
+ * required (without one both are ignored). dx [rows, in], dweight [out, in] contiguous and dbias
+ * [out]: any subset, at least one of the three or, with an activation, none.
  * x is needed for dweight, weight for dx. dweight and dbias are of grad_dtype (s->dtype or
  * ZERO_F32), e.g. inside a replica row that zero_reduce_shard will sum; with accumulate != 0 the
  * sum is added to what they hold (in fp32, then rounded once). rows == 0 zeroes dweight and dbias

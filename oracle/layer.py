@@ -41,7 +41,8 @@ def act(z: np.ndarray, kind: str) -> np.ndarray:
 
 
 def act_slope(z: np.ndarray, kind: str) -> np.ndarray:
-    z = np.asarray(z, np.float64)
+    """The slope; at an infinity its limit, 0 or 1."""
+    z = np.clip(np.asarray(z, np.float64), -1e18, 1e18)  # both are reached long before; keeps a NaN
     if kind == "relu":
         return (z > 0).astype(np.float64)
     if kind == "gelu":

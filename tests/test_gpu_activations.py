@@ -93,3 +93,33 @@ def test_every_value_relative_to_itself(kind, dtype):
     torch.cuda.synchronize()
     want, err = slope_bound(z, kind)
     hold(dz.double().cpu().numpy(), want, err, dtype, "dz", z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", [k for k in L.ACTS if k != "none"])
+def test_slopes_of_far_values(kind, dtype):
+    """Every value beyond 12, up to the type's largest, and the infinities that an overflow of the
+    pre-activation's type leaves: the slope goes to 1 and 0, and is no NaN. A NaN stays one."""
+    banner(f"far slopes {kind} {dtype}")
+    z = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(DT[dtype])
+    zt = z[~torch.isnan(z.float()) & (z.float().abs() > 12.0)].to(DEV)
+    assert int(torch.isinf(zt).sum()) == 2
+    z, m, n = zt.double().cpu().numpy(), zt.numel(), 8
+    pre = zt[:, None].expand(m, n).contiguous()
+    dz, dx = torch.empty_like(pre), torch.empty(m, 1, dtype=zt.dtype, device=DEV)
+    x, w = torch.ones(m, 1, dtype=zt.dtype, device=DEV), torch.ones(n, 1, dtype=zt.dtype, device=DEV)
+    ws = torch.empty(max(16, Z.zero_linear_workspace_bytes(m, 1, n, True)), dtype=torch.uint8, device=DEV)
+    Z.zero_linear_backward(torch.ones_like(pre), x, w, act=kind, pre=pre, dz=dz, dx=dx, workspace=ws)
+    torch.cuda.synchronize()
+    near = np.clip(z, -1e18, 1e18)                    # the bounds' own terms stay finite
+    want, err = slope_bound(near, kind)
+    assert np.array_equal(want, np.clip(L.act_slope(z, kind), -9, 9))
+    got = dz.double().cpu().numpy()
+    far = np.abs(z) > 200                             # where even silu's slope is a whole number
+    assert (got[far] == (z[far] > 0)[:, None]).all()
+    hold(got, want, np.where(far, 0.0, err), dtype, "dz", z)
+    assert bool(torch.isfinite(dx).all())
+    pre.fill_(float("nan"))
+    Z.zero_linear_backward(torch.ones_like(pre), x, w, act=kind, pre=pre, dz=dz, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(dz).all())

@@ -135,3 +135,10 @@ def test_activations_keep_their_digits_far_out(kind):
     }[kind]
     assert (np.abs(L.act(z, kind) - y) <= 1e-12 * np.abs(y)).all()
     assert (np.abs(L.act_slope(z, kind) - (first + second)) <= 1e-12 * (first + np.abs(second))).all()
+
+
+@pytest.mark.parametrize("kind", [k for k in L.ACTS if k != "none"])
+def test_slopes_far_out_are_their_limits(kind):
+    z = np.array([-np.inf, -3e38, -1e20, -1e4, 1e4, 1e20, 3e38, np.inf, np.nan])
+    got = L.act_slope(z, kind)
+    assert np.array_equal(got[:8], [0, 0, 0, 0, 1, 1, 1, 1]) and (kind == "relu" or np.isnan(got[8]))

@@ -56,8 +56,13 @@ __device__ __forceinline__ float act(float z) {
   return z;
 }
 
+// The slope. Past 1000 every one is 0 or 1 in fp32 already; beyond, and at the infinities that an overflow of the
+// stored type leaves, its second term would multiply 0 by an infinity. Keeps a NaN.
+constexpr float kFar = 1000.0f;
+
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
+  z = z > kFar ? kFar : (z < -kFar ? -kFar : z);
   if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == ZERO_ACT_GELU) {
     const Normal n = normal(z);
