@@ -11,7 +11,7 @@
 // Memory is the bound: the loss alone and the gradient alone read the row once, and the step keeps the
 // row in registers between the two, as far as it fits (a row of 131072 16-bit or 65536 fp32 logits);
 // longer rows are read twice, the second time mostly from cache. Measured, with what a large copy reaches
-// 5.1 TB/s: 8192 x 32000 bf16 loss and gradient 210 us (5.0 TB/s), 4096 x 50257 bf16 192 us (4.3, its rows lie off
+// 5.1 TB/s: 8192 x 32000 bf16 loss and gradient 204 us (a tenth of the rows masked), 4096 x 50257 bf16 192 us (4.3, its rows lie off
 // 16 bytes), 4096 x 32000 bf16 loss alone 46 us (5.7), 1024 x 50257 fp32 with a tail 114 us (3.6: rows of
 // 201 kB leave one or two to a CU, so loads, arithmetic and stores overlap less), one row of 50257 9.1 us, which is its chain
 // of loads and reductions.
@@ -225,6 +225,24 @@ __device__ __forceinline__ void add(const Args& a, MaxSum& r, float (&f)[N], uin
   for (int j = 0; j < N; ++j) r.s += ex2(mul_s<T>(a, f[j] - r.m));
 }
 
+// What a row without weight or teacher leaves.
+template <int MODE>
+__device__ __forceinline__ void no_loss(const Args& a, uint64_t row, int t) {
+  if (!(MODE & 1) || t) return;
+  a.loss[row] = 0.0f;
+  if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
+}
+
+template <typename T, int NT>
+__device__ __forceinline__ void no_gradient(T* dz, uint32_t vocab, int t) {
+  using V = typename Pack<T>::type;
+  constexpr uint32_t W = Pack<T>::n;
+  const uint32_t body = vocab / W, last = body * W + t;
+  V zero = {};
+  for (uint32_t i = t; i < body; i += NT) *reinterpret_cast<V*>(dz + (uint64_t)i * W) = zero;
+  if (last < vocab) dz[last] = (T)0.0f;
+}
+
 // NV: 16-byte vectors of the row that a thread of the step holds in registers; 0: reads it again.
 // STREAM: the gradient goes past the caches.
 template <typename T, bool TAIL, int MODE, int NV, int NT, bool STREAM>
@@ -249,8 +267,14 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
   float* s_y = reinterpret_cast<float*>(lds + words + K);
   float* s_z = reinterpret_cast<float*>(lds + words + 2 * K);
 
-  // in the order of need: the row's weight, the teacher's entries, the row
+  // the weight first, and nothing else of the row if it is 0
   const float w = in.weight ? in.weight[row] : 1.0f;
+  if (w == 0.0f) {
+    no_loss<MODE>(a, row, t);
+    if (MODE & 2) no_gradient<T, NT>(dz, vocab, t);
+    return;
+  }
+  // in the order of need: the teacher's entries, the row
   Entry first{-1, 0.0f};
   if (t < 64 && t < (int)K) first = load_entry(in, row, t);
   V held[NV ? NV : 1];
@@ -259,18 +283,6 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
     if (i * NT + t < (int)body) held[i] = *reinterpret_cast<const V*>(z + (uint64_t)(i * NT + t) * W);
   for (uint32_t i = t; i < words / 4; i += NT)
     reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
-  if (w == 0.0f) {
-    if ((MODE & 1) && t == 0) {
-      a.loss[row] = 0.0f;
-      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
-    }
-    if (MODE & 2) {
-      V zero = {};
-      for (uint32_t i = t; i < body; i += NT) *reinterpret_cast<V*>(dz + (uint64_t)i * W) = zero;
-      if (last < vocab) dz[last] = (T)0.0f;
-    }
-    return;
-  }
   __syncthreads();
   if (wave == 0) teach<T, TAIL>(a, row, first, z, bits, s_idx, s_y, s_z, &teacher);
   if (TAIL) __syncthreads();  // the sum needs to know what is listed
@@ -313,15 +325,8 @@ __global__ __launch_bounds__(NT) void k_distill(Args a) {
   }
   __syncthreads();
   if (teacher.none) {
-    if ((MODE & 1) && t == 0) {
-      a.loss[row] = 0.0f;
-      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
-    }
-    if (MODE & 2) {
-      V zero = {};
-      for (uint32_t i = t; i < body; i += NT) *reinterpret_cast<V*>(dz + (uint64_t)i * W) = zero;
-      if (last < vocab) dz[last] = (T)0.0f;
-    }
+    no_loss<MODE>(a, row, t);
+    if (MODE & 2) no_gradient<T, NT>(dz, vocab, t);
     return;
   }
   if (MODE & 1) {
