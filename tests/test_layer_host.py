@@ -180,3 +180,19 @@ def test_sizes_past_the_launch_limit_are_refused():
     assert _fwd(_shape(rows=(1 << 27) + 1)) == OVERFLOW
     assert _fwd(_shape(n=(1 << 27) + 1)) == OVERFLOW and _fwd(_shape(k=(1 << 27) + 1)) == OVERFLOW
     assert Z.zero_linear_workspace_bytes((1 << 27) + 1, 8, 8) == 0
+
+
+def test_binding_takes_none_for_what_a_backward_does_not_read():
+    """None passes the binding's own checks of x and weight: what refuses these calls is the host memory
+    of dy, and a tensor of another shape or kind is still refused for itself."""
+    dy = torch.zeros(4, 6, dtype=torch.bfloat16)
+    x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(6, 8, dtype=torch.bfloat16)
+    for kw in (dict(x=x, weight=None, dweight=w), dict(x=None, weight=w, dx=x), dict(x=None, weight=None, dbias=dy[0]),
+               dict(x=None, weight=None, act="silu", pre=dy, dz=dy)):
+        with pytest.raises(TypeError, match="dy must be a device tensor"):
+            Z.zero_linear_backward(dy, **kw)
+    for kw in (dict(x=x[0], weight=None, dweight=w), dict(x=None, weight=w[0], dx=x), dict(x=None, weight=None, dx=[1])):
+        with pytest.raises(TypeError, match="2-D"):
+            Z.zero_linear_backward(dy, **kw)
+    with pytest.raises(TypeError, match="dy must be a 2-D"):
+        Z.zero_linear_backward(None, x, w)

@@ -611,14 +611,13 @@ def _workspace(t, here: int):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _linear_shape(weight, rows: int, act) -> ZeroLinearShape:
+def _linear_shape(dtype, rows: int, k: int, n: int, act) -> ZeroLinearShape:
     kind = _ACTS.get(act, act)
     if not isinstance(kind, int):
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(_ACTS)}")
-    if weight.dtype is not torch.bfloat16 and weight.dtype is not torch.float16:
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError("the linear layer takes bfloat16 or float16")
-    n, k = weight.shape
-    return ZeroLinearShape(rows, k, n, _TORCH_DT[weight.dtype], kind)
+    return ZeroLinearShape(rows, k, n, _TORCH_DT[dtype], kind)
 
 
 def zero_linear_workspace_bytes(rows: int, in_features: int, out_features: int,
@@ -637,8 +636,8 @@ def zero_linear_forward(x, weight, out, bias=None, residual=None, act="none", pr
     if out is None:
         raise TypeError("out must be a device tensor")
     dt, here, M = weight.dtype, _here(), x.shape[0]
-    s = _linear_shape(weight, M, act)
-    K, N = s.in_features, s.out_features
+    N, K = weight.shape
+    s = _linear_shape(dt, M, K, N, act)
     _check(lib().zero_linear_forward(
         ctypes.byref(s), *_mat(x, M, K, "x", dt, here), _param(weight, N, K, "weight", dt, here),
         _vec(bias, N, "bias", dt, here), *_mat(residual, M, N, "residual", dt, here),
@@ -650,14 +649,22 @@ def zero_linear_backward(dy, x, weight, act="none", pre=None, dz=None, dx=None, 
                          dbias=None, accumulate: bool = False, workspace=None, stream=None):
     """The gradients of zero_linear_forward. With an activation ``dz`` receives dy * act'(pre) (it may
     be ``dy`` or ``pre`` itself); ``dx`` (rows, in), ``dweight`` (out, in) contiguous and ``dbias``
-    (out), each optional; the last two of weight's dtype or float32, e.g. views of a replica row,
-    and added to with ``accumulate``."""
-    for t in (dy, x, weight):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise TypeError("dy, x and weight must be 2-D device tensors")
-    dt, here, M = weight.dtype, _here(), dy.shape[0]
-    s = _linear_shape(weight, M, act)
-    K, N = s.in_features, s.out_features
+    (out), each optional; the last two of the layer's dtype or float32, e.g. views of a replica row,
+    and added to with ``accumulate``. ``x`` is read for ``dweight`` only and ``weight`` for ``dx``
+    only: where that is not asked for, either may be None (a layer already released)."""
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise TypeError("dy must be a 2-D device tensor")
+    for t in (x, weight, dx, dweight):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 2):
+            raise TypeError("x, weight, dx and dweight must be 2-D device tensors or None")
+    here, M = _here(), dy.shape[0]
+    if weight is not None:
+        dt, (N, K) = weight.dtype, weight.shape
+    else:
+        dt, N = dy.dtype, dy.shape[1]
+        wide = x if x is not None else dx if dx is not None else dweight
+        K = 0 if wide is None else wide.shape[1]
+    s = _linear_shape(dt, M, K, N, act)
     g = dweight if dweight is not None else dbias
     gdt = dt if g is None else g.dtype
     if gdt not in _TORCH_DT:
