@@ -5,25 +5,10 @@
 #include <stdint.h>
 
 #include "zero_act.h"
+#include "zero_gemm_plan.h"
 #include "zero_linear.h"
 
 namespace zero {
-
-constexpr uint32_t kGemmStep = 64;  // k per LDS stage; splits of k are whole stages
-
-// Tile shapes: number, whether operands off 4 bytes may take it, rows, columns, waves along the rows,
-// waves along the columns, groups of such waves that share out the k.
-#define ZERO_GEMM_SHAPES                  \
-  ZERO_SHAPE(0, false, 256, 256, 2, 4, 1) \
-  ZERO_SHAPE(1, true, 128, 256, 2, 4, 1)  \
-  ZERO_SHAPE(2, true, 256, 128, 4, 2, 1)  \
-  ZERO_SHAPE(3, true, 128, 128, 2, 2, 1)  \
-  ZERO_SHAPE(4, true, 64, 256, 1, 4, 1)   \
-  ZERO_SHAPE(5, true, 32, 256, 1, 4, 1)   \
-  ZERO_SHAPE(6, true, 64, 64, 2, 2, 1)    \
-  ZERO_SHAPE(7, false, 256, 192, 2, 4, 1) \
-  ZERO_SHAPE(8, false, 192, 256, 2, 4, 1) \
-  ZERO_SHAPE(9, true, 64, 64, 2, 2, 2)
 
 struct GemmDev {
   const void *a, *b, *bias, *res;

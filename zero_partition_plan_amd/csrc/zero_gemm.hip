@@ -1,7 +1,6 @@
-// Matrix products of the linear layer on gfx950: which kernel takes a product, the kernel for a few
-// rows, and the join of a product split over k. The tile kernels are in zero_gemm_kernels.hip.
+// Matrix products of the linear layer on gfx950: the kernel for a few rows, the join of a product split over
+// k, and the launch. Which tile takes a product: zero_gemm_plan.h; the tile kernels: zero_gemm_kernels.hip.
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
 #include "zero_gemm.h"
@@ -138,64 +137,6 @@ hipError_t run_few(const GemmDev& d, hipStream_t s) {
   return hipGetLastError();
 }
 
-// What a tile of each shape takes, in us on MI355X: besides its steps (start and epilogue) with the
-// card almost empty and full, and a step (64 k) with the card almost empty and with `per_cu` tiles on
-// every CU. Fitted to products of 16 to 4096 rows, 768 to 50256 columns and k of 16 to 11008:
-// tiles of 128 x 128 and less win where there are few, as the part besides the steps is shorter
-// (333 x 2304 over k 768: 6.4 us against 20), tiles of 256 x 256 where there are many, as they read
-// least (4096 x 11008 over 4096: 281 us against 311), those of 192 where 256 leave CUs idle (2048 x 5120
-// over 5120: 87 us against 102), two groups of waves on a tile where few tiles walk a long k (1001 x 768
-// over 2304: 15.0 us against 20.6; four groups a tile gain less than 1% more over all). Measured on operands that
-// another kernel has just written: a step of few tiles takes up to twice as long there as on warm ones.
-// `groups` share a tile's steps, so a step counts once for all of them.
-struct TileShape {
-  uint32_t bm, bn, per_cu, groups;
-  float rest_alone, rest_full, alone, full;
-};
-constexpr TileShape kShapes[] = {{256, 256, 1, 1, 8.2f, 13.0f, 1.00f, 1.29f}, {128, 256, 1, 1, 5.8f, 5.8f, 0.62f, 0.95f},
-                                 {256, 128, 1, 1, 5.9f, 8.0f, 0.64f, 0.95f},  {128, 128, 2, 1, 5.1f, 5.1f, 0.40f, 0.88f},
-                                 {64, 256, 2, 1, 5.2f, 5.2f, 0.46f, 1.00f},   {32, 256, 2, 1, 3.9f, 3.9f, 0.43f, 0.80f},
-                                 {64, 64, 5, 1, 3.5f, 3.4f, 0.28f, 0.88f},    {256, 192, 1, 1, 8.4f, 12.0f, 0.74f, 1.00f},
-                                 {192, 256, 1, 1, 7.4f, 10.0f, 0.78f, 1.05f},  {64, 64, 2, 2, 3.7f, 3.8f, 0.40f, 0.98f}};
-constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
-constexpr uint32_t kCus = 256;
-constexpr uint64_t kMaxTiles = 1u << 23;  // of at most 512 threads: a grid dimension holds 2^32
-
-struct Plan {
-  int shape;
-  uint32_t splits, k_split;
-};
-
-// The shape and the split of k with the least predicted time. By sizes alone: the workspace must
-// not depend on alignment. Every call asks for it, so it tries a dozen splits of each shape and none
-// that would only make more rounds of tiles.
-Plan plan(uint64_t m, uint64_t n, uint64_t k) {
-  static const uint32_t kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
-  const uint32_t steps = k ? (uint32_t)((k + kGemmStep - 1) / kGemmStep) : 1u;
-  Plan best{0, 1, steps * kGemmStep};
-  float best_t = 1e30f;
-  for (int i = 0; i < kNumShapes; ++i) {
-    const TileShape& t = kShapes[i];
-    const uint64_t tiles = ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
-    const float slots = (float)(kCus * t.per_cu);
-    for (const uint32_t sp : kSplits) {
-      if (sp > 1 && (steps / sp < 2 || (float)tiles * (float)sp > 4.0f * slots)) break;
-      const uint32_t turns = (steps + sp * t.groups - 1) / (sp * t.groups);  // steps of a group
-      const uint32_t per = turns * t.groups, splits = (steps + per - 1) / per;
-      const float loads = (float)tiles * (float)splits / slots, rounds = floorf(loads), part = loads - rounds;
-      float time = rounds * (t.rest_full + (float)turns * t.full);
-      if (part > 0.0f) time += t.rest_alone + (float)turns * (t.alone + (t.full - t.alone) * part);
-      // the join's launch, and the partial sums written and read at some 4 TB/s
-      if (splits > 1) time += 3.0f + (float)m * (float)n * (float)splits * 8.0f / 4e6f;
-      if (time < best_t) {
-        best_t = time;
-        best = Plan{i, splits, per * kGemmStep};
-      }
-    }
-  }
-  return best;
-}
-
 // Whether an operand can be loaded straight to LDS: those loads want whole dwords, not 16 bytes (4096 x
 // 4100 x 4100 forward 178 us, 295 through registers). The row pitch keeps a tile's offsets in 32 bits.
 bool direct(const void* p, uint64_t ld) {
@@ -226,15 +167,8 @@ hipError_t gemm(const GemmArgs& g, hipStream_t s) {
 
   const bool dir = direct(g.a, g.lda) && direct(g.b, g.ldb);
   Plan p = plan(g.m, g.n, g.k);
-  if (!dir && (p.shape == 0 || p.shape == 7 || p.shape == 8)) p.shape = 1;  // the same splits and workspace
   uint64_t tiles_m, tiles_n;
-  for (int again = 0;; ++again) {
-    tiles_m = (g.m + (uint64_t)kShapes[p.shape].bm - 1) / kShapes[p.shape].bm;
-    tiles_n = (g.n + (uint64_t)kShapes[p.shape].bn - 1) / kShapes[p.shape].bn;
-    if (tiles_m * tiles_n < kMaxTiles) break;
-    if (again) return hipErrorInvalidConfiguration;
-    p.shape = 1;  // small tiles of a result of 2^35 elements and more: larger ones
-  }
+  if (!place(g.m, g.n, dir, p, tiles_m, tiles_n)) return hipErrorInvalidConfiguration;
   d.tiles_m = (uint32_t)tiles_m, d.tiles_n = (uint32_t)tiles_n;
   d.splits = p.splits, d.k_split = p.k_split;
   hipError_t e;
