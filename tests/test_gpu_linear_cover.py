@@ -6,7 +6,8 @@ import torch
 
 import zero_partition_plan_amd as Z
 from gpu_util import DEV, banner
-from test_gpu_linear import DT, Placed, gen, ints, same, ws
+from linear_shapes import TILES, TOO_MANY_TILES
+from test_gpu_linear import DT, SHARED, SIZES, Placed, gen, ints, same, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,88 @@ def test_backward_without_what_it_does_not_read(m, k, n):
         Z.zero_linear_backward(dy, x, None, dx=dx, workspace=w0)
     with pytest.raises(ValueError):
         Z.zero_linear_backward(dy, x, None, dx=torch.empty(m, k + 1, dtype=dt, device=DEV), workspace=w0)
+
+
+def _exact(a, b):
+    """a b^T of whole numbers, exact in fp32 (sums below 2^24)."""
+    return torch.mm(a.float().contiguous(), b.float().contiguous().t())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("order,shape,split", TILES)
+def test_every_tile_with_all_that_it_writes(order, shape, split, held, dtype):
+    """Each tile of each product, joined over k or not, from operands loaded directly and from ones an element
+    off: forward with bias, activation, residual and the kept pre-activation, and over the residual itself;
+    weight gradients written and added to, 16-bit and fp32. Edges odd (or even, beside them), NaN around every operand."""
+    m, k, n = TILES[order, shape, split]
+    n += held
+    off, pad = (1, 0) if held else (8, "to 8")
+    banner(f"linear tile {order} {shape} split={split} held={held} {dtype} m={m} k={k} n={n}")
+    dt, g, nan = DT[dtype], gen(m + k + n), float("nan")
+    x = Placed(m, k, dt, off, pad, nan).set(ints(g, m, k))
+    w = Placed(n, k, dt, off, 0, nan).set(ints(g, n, k))
+    if order == "fwd":
+        b = Placed(1, n, dt, off, 0, nan).set(ints(g, 1, n))
+        r = Placed(m, n, dt, off, pad).set(ints(g, m, n, 50))
+        y, pre = Placed(m, n, dt, off, pad), Placed(m, n, dt, off, pad)
+        z = _exact(x.t, w.t)
+        Z.zero_linear_forward(x.t, w.t, y.t, workspace=ws(m, k, n))
+        same(y.t, z, "y")
+        z = z + b.t.float()
+        Z.zero_linear_forward(x.t, w.t, y.t, bias=b.t[0], residual=r.t, act="relu", pre=pre.t, workspace=ws(m, k, n))
+        same(y.t, z.clamp_min(0) + r.t.float(), "y of everything")
+        same(pre.t, z, "pre")
+        z = z + r.t.float()
+        Z.zero_linear_forward(x.t, w.t, r.t, bias=b.t[0], residual=r.t, workspace=ws(m, k, n))
+        same(r.t, z, "y in place of the residual")
+        for p, what in ((y, "y"), (pre, "pre"), (r, "residual")):
+            p.check_canary(what)
+        return
+    dy = Placed(m, n, dt, off, pad, nan).set(ints(g, m, n))
+    if order == "dx":
+        dx = Placed(m, k, dt, off, pad)
+        Z.zero_linear_backward(dy.t, None, w.t, dx=dx.t, workspace=ws(m, k, n, True))
+        same(dx.t, _exact(dy.t, w.t.t()), "dx")
+        dx.check_canary("dx")
+        return
+    want = _exact(dy.t.t(), x.t.t())
+    for gdt in (dt, torch.float32):
+        dw, old = Placed(n, k, gdt, off), ints(g, n, k, 40).float()
+        Z.zero_linear_backward(dy.t, x.t, None, dweight=dw.t, workspace=ws(m, k, n, True))
+        same(dw.t, want, "dweight")
+        dw.t.copy_(old)
+        Z.zero_linear_backward(dy.t, x.t, None, dweight=dw.t, accumulate=True, workspace=ws(m, k, n, True))
+        same(dw.t, want + old, "dweight added to")
+        dw.check_canary("dweight")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,k,n", SIZES + SHARED)
+def test_residual_in_place_at_every_size(m, k, n, dtype):
+    banner(f"linear residual in place m={m} k={k} n={n} {dtype}")
+    dt, g = DT[dtype], gen(m + n)
+    x, w = ints(g, m, k).to(dt), ints(g, n, k).to(dt)
+    r = Placed(m, n, dt, 3, 5).set(ints(g, m, n, 50))
+    want = _exact(x, w) + r.t.float()
+    Z.zero_linear_forward(x, w, r.t, residual=r.t, workspace=ws(m, k, n))
+    same(r.t, want, "y in place of the residual")
+    r.check_canary("y")
+
+
+def test_more_tiles_than_a_grid_holds():
+    """A long and narrow result whose 64 x 64 tiles, the planned ones, are past 2^23: it takes larger ones."""
+    m, k, n = TOO_MANY_TILES
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GiB")
+    banner(f"linear more tiles than a grid holds m={m} k={k} n={n}")
+    g = gen(9)
+    x = torch.randint(-3, 4, (m, k), generator=g, device=DEV, dtype=torch.int8).bfloat16()
+    w = ints(g, n, k).bfloat16()
+    y = torch.empty(m, n, dtype=torch.bfloat16, device=DEV)
+    Z.zero_linear_forward(x, w, y, workspace=ws(m, k, n))
+    wt = w.float().t().contiguous()
+    for r in range(0, m, 1 << 22):                 # whole numbers of at most 72: exact in bf16
+        assert torch.equal(y[r:r + (1 << 22)], (x[r:r + (1 << 22)].float() @ wt).bfloat16()), r
+    del y
+    torch.cuda.empty_cache()
