@@ -44,7 +44,7 @@ struct Args {
 enum { kForward = 1, kBackward = 2, kStep = 3 };  // bit 0: loss, bit 1: gradient
 
 // c * d for a difference of logits d, to fp32 accuracy: c in one fp32 number would lose up to
-// 2^-25 |c d| to its own rounding, seen in the small probabilities of an fp32 gradient. -inf is taken
+// 2^-24 |c d| to its own rounding, seen in the small probabilities of an fp32 gradient. -inf is taken
 // as the lowest finite number (c_lo may be negative or 0, and would make a NaN of it); T is at most
 // 2^20, so that is still an exponent far below any fp32.
 __device__ __forceinline__ float mul_c(const Args& a, float d) {
@@ -52,8 +52,10 @@ __device__ __forceinline__ float mul_c(const Args& a, float d) {
   return __builtin_fmaf(d, a.c_hi, d * a.c_lo);
 }
 
-// The same inside the pass over the logits: 16-bit logits, whose gradient is rounded to 16 bits,
-// take the one-term product.
+// The same inside the pass over the logits. 16-bit logits take the one-term product: their gradient is rounded to
+// 16 bits, far above it, and the fp32 loss of such a row is off by at most 2^-24 of the mean of (m - z)/T
+// under q, 6e-7 at a mean of 10, about what the roundings of its logarithms are. The two terms cost 8% of the loss
+// alone (2048 x 131072 fp16 100.5 us against 93.1) and 2 us of the step on one row (11.4 against 9.4).
 template <typename T>
 __device__ __forceinline__ float mul_s(const Args& a, float d) {
   return sizeof(T) == 4 ? mul_c(a, d) : d * a.c_hi;
