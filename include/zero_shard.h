@@ -502,7 +502,8 @@ typedef struct {
  * logit -inf has p = 0. An index listed twice counts with both its p. A row with no teacher mass
  * at all (no entry, all -inf) and a row of weight 0 have loss 0 and gradient 0. Logits of -inf
  * are entries of no mass; a row with a NaN, a +inf or nothing but -inf has no softmax: its
- * loss and gradient are NaN. A loss may be +inf (mass of p where q has none).
+ * loss and gradient are NaN. A NaN or +inf among a row's teacher logits, or a NaN tail, makes its loss
+ * and its listed entries' gradients NaN. A loss may be +inf (mass of p where q has none).
  * loss: device float[rows]. stats: device float[2*rows], what the backward needs of the row
  * (opaque). Sums are fp32 in a fixed order. rows == 0 enqueues nothing.
  * Errors: NULLs, topk or vocab 0, index_bytes not 4 or 8, T out of its range, a leading dimension

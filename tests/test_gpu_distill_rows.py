@@ -155,3 +155,61 @@ def test_masked_rows_are_not_read():
     assert not bool(grad.any()) and not bool(loss.any())
     print(f"[gpu] all rows {full * 1e3:.0f} us, all masked {masked * 1e3:.0f} us", flush=True)
     assert masked <= 0.75 * full
+
+
+@pytest.mark.parametrize("kind", ["step", "calls"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(3, 140003), (520, 140003), (520, 50257), (40, 16001)])
+def test_over_the_logits_themselves(R, V, dtype, kind):
+    """The gradient in place of the logits, rows longer and shorter than the registers hold: bit for bit as apart."""
+    banner(f"distill in place R={R} V={V} {dtype} {kind}")
+    z, idx, top, t, weight = batch(max(R, 8), V, 33, dtype, True, R)
+    z, idx, top, t, weight = (a[:R].contiguous() for a in (z, idx, top, t, weight))
+    out = []
+    for apart in (True, False):
+        logits = z.clone()
+        loss, grad = torch.empty(R, device=DEV), torch.empty_like(z) if apart else logits
+        kw = dict(tail=t, weight=weight)
+        if kind == "step":
+            Z.zero_distill_step(logits, idx, top, 2.0, loss, grad, scale=8.0, **kw)
+        else:
+            stats = torch.empty(R, 2, device=DEV)
+            Z.zero_distill_forward(logits, idx, top, 2.0, loss, stats, **kw)
+            Z.zero_distill_backward(logits, idx, top, 2.0, stats, grad, scale=8.0, **kw)
+        torch.cuda.synchronize()
+        out.append((loss, grad))
+    bits = torch.int32 if dtype == "f32" else torch.int16
+    assert torch.equal(out[0][0].view(torch.int32), out[1][0].view(torch.int32))
+    assert torch.equal(out[0][1].view(bits), out[1][1].view(bits))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("kind", ["step", "calls"])
+def test_a_teacher_without_a_softmax(kind, tail):
+    """A NaN or +inf among the teacher's logits, or a NaN for the tail: the loss and the listed entries' gradients
+    are NaN, so that the overflow flag sees the row; other rows are as without it."""
+    z, idx, top, t, weight = batch(9, 3001, 20, "f32", tail, 2)
+    weight.fill_(1.0)
+    z[3], z[6] = z[0], z[1]
+    clean = None
+    for spoil in (False, True):
+        if spoil:
+            top[0, 7], top[7, 3] = float("nan"), float("inf")
+            if tail:
+                t[8] = float("nan")
+        loss, grad, stats = torch.empty(9, device=DEV), torch.empty_like(z), torch.empty(9, 2, device=DEV)
+        if kind == "step":
+            Z.zero_distill_step(z, idx, top, 1.5, loss, grad, tail=t, weight=weight)
+        else:
+            Z.zero_distill_forward(z, idx, top, 1.5, loss, stats, tail=t, weight=weight)
+            Z.zero_distill_backward(z, idx, top, 1.5, stats, grad, tail=t, weight=weight)
+        torch.cuda.synchronize()
+        if not spoil:
+            clean = loss, grad
+            assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(grad).all())
+    bad = [0, 7] + ([8] if tail else [])
+    good = [r for r in range(9) if r not in bad]
+    assert bool(torch.isnan(loss[bad]).all())
+    for r in bad:
+        assert bool(torch.isnan(grad[r, idx[r][idx[r] >= 0].long()]).all())
+    assert torch.equal(loss[good], clean[0][good]) and torch.equal(grad[good], clean[1][good])

@@ -122,3 +122,67 @@ def test_more_tiles_than_a_grid_holds():
         assert torch.equal(y[r:r + (1 << 22)], (x[r:r + (1 << 22)].float() @ wt).bfloat16()), r
     del y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,unit", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+@pytest.mark.parametrize("m,k,n", [(3, 72, 40), (100, 200, 136), (700, 264, 520)])
+def test_subnormal_operands(m, k, n, dtype, unit):
+    """Whole multiples of the type's smallest number: what gradients below a loss scale come to. Exact as the
+    whole numbers are, in the products, the sums, the 16-bit results and the bias gradient."""
+    banner(f"linear subnormal {dtype} m={m} k={k} n={n}")
+    dt, g = DT[dtype], gen(m)
+    x, dy = (ints(g, *s, 9) * unit for s in ((m, k), (m, n)))
+    w = ints(g, n, k)
+    xt, dt_, wt = x.to(dt), dy.to(dt), w.to(dt)
+    assert torch.equal(xt.double(), x) and torch.equal(dt_.double(), dy)
+    y, dx, dw, db = (torch.empty(s, dtype=dt, device=DEV) for s in ((m, n), (m, k), (n, k), (n,)))
+    Z.zero_linear_forward(xt, wt, y, workspace=ws(m, k, n))
+    one = torch.ones(m, k, dtype=dt, device=DEV)
+    Z.zero_linear_backward(dt_, one, wt, dx=dx, dweight=dw, dbias=db, workspace=ws(m, k, n, True))
+    same(y, (x.cpu() @ w.cpu().t()).to(DEV), "y")
+    same(dx, (dy.cpu() @ w.cpu()).to(DEV), "dx")
+    same(db, dy.sum(0), "dbias")
+    same(dw, dy.sum(0)[:, None].expand(n, k), "dweight")
+
+
+_FIRST = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import zero_partition_plan_amd as Z
+dev = "cuda:0"
+m, k, n = 2048, 2048, 8192          # tiles of more LDS than a kernel has without asking
+x, w, dy = (torch.randint(-3, 4, s, device=dev).bfloat16() for s in ((m, k), (n, k), (m, n)))
+y, dx, dw = torch.empty(m, n, dtype=torch.bfloat16, device=dev), torch.empty_like(x), torch.empty(n, k, device=dev)
+z = torch.randn(64, 5000, device=dev)
+idx, top, loss, grad = torch.randint(5000, (64, 4), device=dev), torch.randn(64, 4, device=dev), torch.empty(64, device=dev), torch.empty_like(z)
+ws = torch.empty(max(16, *(Z.zero_linear_workspace_bytes(m, k, n, b) for b in (False, True))), dtype=torch.uint8, device=dev)
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    Z.zero_linear_forward(x, w, y, workspace=ws)
+    Z.zero_linear_backward(dy, x, w, dx=dx, dweight=dw, workspace=ws)
+    Z.zero_distill_step(z, idx, top, 1.0, loss, grad)
+for _ in range(3):
+    for t in (y, dx, dw, loss, grad):
+        t.fill_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, dx, dw, loss, grad)]
+    Z.zero_linear_forward(x, w, y, workspace=ws)
+    Z.zero_linear_backward(dy, x, w, dx=dx, dweight=dw, workspace=ws)
+    Z.zero_distill_step(z, idx, top, 1.0, loss, grad)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, dx, dw, loss, grad)))
+    assert torch.equal(y.float(), (x.float() @ w.float().t()).bfloat16().float())
+print("captured first")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """Nothing of the library's kernels loaded or allowed before the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _FIRST, root], capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0 and "captured first" in run.stdout, (run.stdout + run.stderr)[-3000:]
