@@ -10,11 +10,11 @@
 //
 // Memory is the bound: the loss alone and the gradient alone read the row once, and the step keeps the
 // row in registers between the two, as far as it fits (a row of 131072 16-bit or 65536 fp32 logits);
-// longer rows are read twice, the second time mostly from cache. Measured, with what a large copy reaches
-// 5.1 TB/s: 8192 x 32000 bf16 loss and gradient 204 us (a tenth of the rows masked), 4096 x 50257 bf16 192 us (4.3, its rows lie off
-// 16 bytes), 4096 x 32000 bf16 loss alone 46 us (5.7), 1024 x 50257 fp32 with a tail 114 us (3.6: rows of
-// 201 kB leave one or two to a CU, so loads, arithmetic and stores overlap less), one row of 50257 9.1 us, which is its chain
-// of loads and reductions.
+// longer rows are read twice, the second time mostly from cache. Measured on inputs that change from pass to
+// pass, where a large copy reaches 6.1 TB/s and reading alone 7.1: 8192 x 32000 bf16 loss and gradient 204 us (5.1 TB/s),
+// 4096 x 50257 bf16 191 us (4.3, its rows lie off 16 bytes), 4096 x 32000 bf16 loss alone 52 us (5.1), 2048 x
+// 131072 fp16 loss alone 99 us (5.4), 1024 x 50257 fp32 with a tail 116 us (3.5: rows of 201 kB leave one or two
+// to a CU, so loads, arithmetic and stores overlap less), one row of 50257 9.3 us, which is its chain of loads and reductions.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -39,8 +39,8 @@ __global__ __launch_bounds__(256) void k_join(GemmDev g) {
 // is to do: 16 of its rows a block, straight from memory into the matrix instruction's registers,
 // the waves taking turns along k and joined through LDS in their order. No split over blocks, so
 // one launch. Any alignment; rows past the end repeat the last one and are not stored. Bound by the
-// loads in flight: 8 of a wave and 8 waves a CU on 4096 x 4096, 33.6 MB in 7.7 us (4.4 TB/s); the split
-// tile kernel and its join took 12.
+// loads in flight: 8 of a wave and 8 waves a CU on 4096 x 4096, 33.6 MB in 8.9 us (3.8 TB/s; 7.6 us if it was
+// read just before); the split tile kernel and its join took 12.
 template <typename T, int MT>
 __global__ __launch_bounds__(1024) void k_few(GemmDev g) {
 #if defined(__HIP_DEVICE_COMPILE__)

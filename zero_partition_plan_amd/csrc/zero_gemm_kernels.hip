@@ -9,8 +9,8 @@
 // read from LDS as it lies, a k-major one (dz and the weight in dz W, both operands of dz^T x) by the transposing
 // LDS read, so no operand is ever transposed in memory.
 //
-// What bounds it is the clock under load and the waits between products: on 8192^3 random bf16 the 256 x 256 tile reaches 1360 to 1410 (x W^T), 1380 to
-// 1460 (dz W) and 1440 to 1500 TFLOP/s (dz^T x), from card to card, at 1.5 to
+// What bounds it is the clock under load and the waits between products: on 8192^3 random bf16 the 256 x 256 tile reaches 1360 to 1420 (x W^T), 1380 to
+// 1510 (dz W) and 1440 to 1520 TFLOP/s (dz^T x), from card to card, at 1.5 to
 // 1.6 GHz with the matrix units busy in 72, 73 and 78% of the cycles, on zeros 1540 to 1710; hence the instruction with the
 // fewest trips of the sums through the matrix unit (the 32x32x16 one: 5 to 9% less), and two stages of
 // 64 k rather than more of 32 (a second barrier per 64 k: 14 to 23% less). 8 waves of 128 x 64 sums
