@@ -16,7 +16,7 @@ constexpr uint64_t kMaxSize = 1u << 27;  // keeps every grid below 2^32 threads 
 // dz = round16(dy * act'(pre)), 8 columns a thread, and the bias gradient's partial sums of the
 // stored dz: a block takes 256 columns and `chunk` rows, its 8 threads on a column every eighth row,
 // joined through LDS in a fixed order. One pass over dy and pre: memory is the bound. Without an
-// activation only the sums are formed. 333 x 2304 fp16 with gelu_tanh and its join: 4.3 to 5.0 and 2.0 to 2.7 us (one
+// activation only the sums are formed. 333 x 2304 fp16 with gelu_tanh and its join: 4.3 to 5.1 and 2.0 to 2.9 us (one
 // thread a column over all rows took 80).
 constexpr int kColsPerBlock = 256, kRowLanes = 8;
 
