@@ -319,6 +319,83 @@ zero_status zero_adam_shard_step_dev_t(const zero_grad_src* src, uint64_t n,
                                        void* out_param, int32_t out_dtype, const int32_t* d_skip,
                                        void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The update of many tensors in one call, for parameters that are not one flat shard or whose decay
+ * differs from tensor to tensor, with Adam's moments in 32 bits or in 8.
+ *
+ * A moment in 8 bits: each run of ZERO_STATE8_BLOCK elements of a tensor (the last one may be shorter)
+ * keeps one fp32 scale s, the largest magnitude in it, and one byte for each element, an index into
+ * values spaced as squares. With T = 127 for the first moment m (signed, int8) and T = 255 for the
+ * second, held as its root w = sqrt(v) (unsigned, uint8):
+ *   value(q) = (q*|q|) * f32(s * f32(1/T^2));  v = w*w
+ * and x is stored as the index, with x's sign, of
+ *   t = f32(f32(|x| * f32(1/s)) * T^2);  q = the smallest integer >= 0 with t <= (q + 1/2)^2
+ * that is, the value nearest in square root, halves down; a w above 0 is at least q = 1. The step is
+ * 1.6% of the largest for m and 0.8% for w there, and the smallest value 6e-5 and 1.5e-5 of it. A block whose
+ * largest is below 2^-126 keeps s = 0 (all zeros), one with a non-finite value s = NaN (all NaN).
+ * Zeroed bytes and scales are the state of a new parameter. Every operation is fp32, rounded to nearest
+ * even on its own, so equal inputs give equal bytes. */
+#define ZERO_STATE8_BLOCK 256
+#define ZERO_ADAM_MAX_TENSORS 65536 /* tensors of one call */
+#define ZERO_ADAM_MAX_GROUPS 16     /* sets of hyper-parameters of one call */
+
+typedef struct {
+  uint64_t n;       /* elements; 0 is an empty entry, its arrays may be NULL */
+  float* param;     /* device float[n]: the fp32 parameters, updated in place */
+  const void* grad; /* device [n] of the call's grad_dtype */
+  void* out_param;  /* device 16-bit [n] or NULL: the updated parameters, rounded to nearest even */
+  void* m;          /* device float[n], or with state_bits 8 int8_t[n] */
+  void* v;          /* device float[n], or with state_bits 8 uint8_t[n] */
+  float* m_scale;   /* state_bits 8: device float[ceil(n / ZERO_STATE8_BLOCK)]; else NULL */
+  float* v_scale;
+  uint32_t group;      /* which of the call's hyper-parameters */
+  uint32_t state_bits; /* 32 or 8 */
+} zero_adam_tensor;
+
+/* One Adam/AdamW step of each of `count` tensors (P1 section 二: a rank updates its own parameters
+ * with its own state): for every element the update of zero_adam_shard_step with the single replica
+ * `grad`, the constants of its tensor's group (zero_adam_derive of groups[group]) and the grad scale
+ * *d_grad_scale if that is given (device float, as zero_clip_scale writes it), else grad_scale. A tensor
+ * of 32-bit state ends with the bits zero_adam_shard_step gives. One of 8-bit state reads its moments'
+ * values, updates the parameter from the new moments before they are rounded, and stores those.
+ * The groups share one wd_mode. `tensors` and `groups` are host arrays, read before the call returns.
+ * out_dtype (ZERO_BF16 or ZERO_F16) is that of every out_param. d_skip as in zero_adam_shard_step.
+ * Any number of tensors takes one launch for each 48 of the same state_bits.
+ * Aliasing: an array that is written (param, m, v, scales, out_param) overlaps no array or word of the call, of any
+ * tensor; gradients may be shared. Every array at any multiple of its element size.
+ * Errors: NULLs, group >= ngroups, state_bits not 32 or 8, ngroups outside 1..ZERO_ADAM_MAX_GROUPS (with
+ * count 0 too), bad or mixed hyper-parameters, scales with 32-bit state, aliasing, an array not naturally aligned ->
+ * ZERO_E_INVAL; out_dtype ZERO_F32 with an out_param, count above ZERO_ADAM_MAX_TENSORS ->
+ * ZERO_E_UNSUPPORTED; n*8 >= 2^64 -> ZERO_E_OVERFLOW. */
+zero_status zero_adam_tensors_step(const zero_adam_tensor* tensors, uint32_t count,
+                                   int32_t grad_dtype, int32_t out_dtype,
+                                   const zero_adam_hparams* groups, uint32_t ngroups,
+                                   float grad_scale, const float* d_grad_scale,
+                                   const int32_t* d_skip, void* stream);
+
+/* zero_adam_tensors_step with its step counter in device memory, as zero_adam_shard_step_dev_t keeps
+ * it: constants of group k at step t = *d_step from d_table[k*table_len + t - 1] (device
+ * zero_adam_scalars[ngroups*table_len]), one advance of *d_step for the whole call, a t outside the
+ * table refused in *d_status with nothing written. With nothing to update only the advance is enqueued.
+ * Errors: as zero_adam_tensors_step and zero_adam_shard_step_dev_t. */
+zero_status zero_adam_tensors_step_dev_t(const zero_adam_tensor* tensors, uint32_t count,
+                                         int32_t grad_dtype, int32_t out_dtype,
+                                         const float* d_grad_scale, const zero_adam_scalars* d_table,
+                                         uint32_t ngroups, uint32_t table_len, int64_t* d_step,
+                                         int32_t* d_status, int32_t wd_mode, const int32_t* d_skip,
+                                         void* stream);
+
+/* The numbers that an 8-bit moment stands for, in fp32, and the moment that fp32 numbers make: for
+ * checkpoints, and for a state that moves between 8 and 32 bits (P1 section 一: the optimizer state of a
+ * parameter). moment: 1 (m, int8 codes) or 2 (v itself, not its root; uint8 codes; v is not negative, and where
+ * it is the block becomes NaN). codes: device [n]; scale: device float[ceil(n/256)]; values: device float[n].
+ * Aliasing: the arrays of a call must not overlap. Errors: NULLs, another moment, aliasing, an array not
+ * naturally aligned -> ZERO_E_INVAL; n*8 >= 2^64 -> ZERO_E_OVERFLOW. */
+zero_status zero_adam_state_values(const void* codes, const float* scale, uint64_t n,
+                                   int32_t moment, float* values, void* stream);
+zero_status zero_adam_state_codes(const float* values, uint64_t n, int32_t moment, void* codes,
+                                  float* scale, void* stream);
+
 /* Gradient-clipping scale for the two-pass step, formed on the device. The pages do not clip; this
  * is the usual global-norm rule, with the shard's squared norm standing for the global one:
  *   q = max_norm / (sqrt(*d_sq) + clip_eps)       fp64, each operation correctly rounded

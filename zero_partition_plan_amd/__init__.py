@@ -29,6 +29,9 @@ __all__ = [
     "zero_adam_shard_step_dev_scale", "zero_clip_scale", "zero_adam_derive_table", "adam_table",
     "zero_adam_shard_step_dev_t",
     "AdamStep", "ReduceCall",
+    "ZeroAdamTensor", "ZERO_STATE8_BLOCK", "ZERO_ADAM_MAX_TENSORS", "ZERO_ADAM_MAX_GROUPS", "adam_tensor",
+    "adam_state", "zero_adam_tensors_step", "zero_adam_tensors_step_dev_t", "AdamTensorsStep",
+    "zero_adam_state_values", "zero_adam_state_codes",
     "zero_gather_params", "zero_host_adam_step", "zero_offload_step",
     "ZeroLinearShape", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_GELU_TANH",
     "ZERO_ACT_SILU", "zero_linear_workspace_bytes", "zero_linear_forward", "zero_linear_backward",
@@ -48,6 +51,10 @@ ZERO_DISTILL_MAX_TOPK = 1024
 ZERO_DISTILL_MAX_VOCAB = 393216
 ZERO_STATIC_SQ_PARTIALS = 4 << 20
 ZERO_STATIC_MAX_ELEMS = (ZERO_STATIC_SQ_PARTIALS - 1024) * 256
+
+ZERO_STATE8_BLOCK = 256
+ZERO_ADAM_MAX_TENSORS = 65536
+ZERO_ADAM_MAX_GROUPS = 16
 
 _TORCH_DT = {torch.float32: ZERO_F32, torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16}
 
@@ -98,6 +105,12 @@ class ZeroArenaArray(ctypes.Structure):
 
 class ZeroAdamScalars(ctypes.Structure):
     _fields_ = [(k, ctypes.c_float) for k in ("b1", "b2", "c1", "c2", "ss", "bc", "e", "dec", "w")]
+
+
+class ZeroAdamTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_uint64)] + [(k, ctypes.c_void_p) for k in (
+        "param", "grad", "out_param", "m", "v", "m_scale", "v_scale")] + [
+        ("group", ctypes.c_uint32), ("state_bits", ctypes.c_uint32)]
 
 
 class ZeroLinearShape(ctypes.Structure):
@@ -159,6 +172,12 @@ def lib() -> ctypes.CDLL:
             "zero_adam_derive_table": [P(ZeroAdamHParams), u32, P(ZeroAdamScalars)],
             "zero_adam_shard_step_dev_t": [P(_GradSrc), u64, vp, vp, u32, vp, vp, i32, vp, vp, vp,
                                            vp, i32, vp, vp],
+            "zero_adam_tensors_step": [P(ZeroAdamTensor), u32, i32, i32, P(ZeroAdamHParams), u32,
+                                       ctypes.c_float, vp, vp, vp],
+            "zero_adam_tensors_step_dev_t": [P(ZeroAdamTensor), u32, i32, i32, vp, vp, u32, u32, vp,
+                                             vp, i32, vp, vp],
+            "zero_adam_state_values": [vp, vp, u64, i32, vp, vp],
+            "zero_adam_state_codes": [vp, u64, i32, vp, vp, vp],
             "zero_gather_params": [P(vp), u32, u64, u32, u64, u64, vp, vp],
             "zero_host_adam_step": [vp, u64, ctypes.c_float, vp, vp, vp, P(ZeroAdamHParams), vp, i32,
                                     u32],
@@ -733,6 +752,151 @@ def zero_distill_step(logits, top_index, top_logits, temperature: float, loss, d
         ctypes.byref(a), _vec(upstream, a.rows, "upstream", f32, here), float(scale),
         _vec(loss, a.rows, "loss", f32, here), *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype, here),
         _stream_on(stream, here)), "zero_distill_step")
+
+
+# ------------------------------------------------------------------------------ the update of many tensors
+
+class _Tensors:
+    """A list of tensors marshalled for zero_adam_tensors_step: the entries, their common types, and what
+    keeps their memory alive."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        self.count, self.keep = len(tensors), tensors
+        self.array = (ZeroAdamTensor * max(1, self.count))(*[t[0] for t in tensors])
+        gdts = {t[1]["grad"].dtype for t in tensors}
+        odts = {t[1]["out"].dtype for t in tensors if t[1]["out"] is not None}
+        if len(gdts) > 1 or len(odts) > 1:
+            raise TypeError("the gradients of a call share one dtype, and so do its out tensors")
+        self.grad_dtype = _TORCH_DT[gdts.pop()] if gdts else ZERO_F32
+        self.out_dtype = _TORCH_DT[odts.pop()] if odts else ZERO_F32
+        devices = {t[1]["param"].get_device() for t in tensors}
+        if len(devices) > 1:
+            raise ValueError("the tensors of a call must be on one device")
+        self.device = devices.pop() if devices else None
+
+    def check_device(self):
+        if self.device is not None and self.device != _here():
+            raise ValueError(f"the tensors are on cuda:{self.device}, the current device is cuda:{_here()}")
+
+
+def adam_tensor(param, grad, m, v, out=None, m_scale=None, v_scale=None, group: int = 0):
+    """One tensor of zero_adam_tensors_step: ``param`` float32, ``grad`` float32, bfloat16 or float16, ``m`` and
+    ``v`` float32, or int8 and uint8 with their scales (as adam_state makes them), ``out`` the 16-bit copy or
+    None. Contiguous device tensors of any shape with as many elements as ``param`` each."""
+    if not isinstance(param, torch.Tensor):
+        raise TypeError("param must be a device tensor")
+    n, here = param.numel(), param.get_device()
+    eight = isinstance(m, torch.Tensor) and m.dtype is torch.int8
+    blocks = -(-n // ZERO_STATE8_BLOCK)
+    if eight and (m_scale is None or v_scale is None):
+        raise TypeError("8-bit states need m_scale and v_scale")
+    if not eight and (m_scale is not None or v_scale is not None):
+        raise TypeError("scales belong to 8-bit states")
+    gdt = grad.dtype if isinstance(grad, torch.Tensor) and grad.dtype in _TORCH_DT else torch.float32
+    odt = out.dtype if isinstance(out, torch.Tensor) and out.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16
+    f32 = torch.float32
+    for t, what in ((grad, "grad"), (m, "m"), (v, "v")):
+        if t is None:
+            raise TypeError(f"{what} must be a device tensor")
+    entry = ZeroAdamTensor(
+        n, _vec(param, n, "param", f32, here), _vec(grad, n, "grad", gdt, here), _vec(out, n, "out", odt, here),
+        _vec(m, n, "m", torch.int8 if eight else f32, here), _vec(v, n, "v", torch.uint8 if eight else f32, here),
+        _vec(m_scale, blocks, "m_scale", f32, here), _vec(v_scale, blocks, "v_scale", f32, here), int(group),
+        8 if eight else 32)
+    return entry, {"param": param, "grad": grad, "out": out, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale}
+
+
+def adam_state(param, bits: int = 32) -> dict:
+    """The state of a new parameter, as keyword arguments of adam_tensor."""
+    if bits == 32:
+        return {"m": torch.zeros_like(param, dtype=torch.float32), "v": torch.zeros_like(param, dtype=torch.float32)}
+    if bits != 8:
+        raise ValueError("states have 32 or 8 bits")
+    blocks = -(-param.numel() // ZERO_STATE8_BLOCK)
+    scale = torch.zeros((2, blocks), dtype=torch.float32, device=param.device)
+    return {"m": torch.zeros(param.shape, dtype=torch.int8, device=param.device),
+            "v": torch.zeros(param.shape, dtype=torch.uint8, device=param.device),
+            "m_scale": scale[0], "v_scale": scale[1]}
+
+
+def _groups(groups):
+    groups = [groups] if isinstance(groups, ZeroAdamHParams) else list(groups)
+    return (ZeroAdamHParams * max(1, len(groups)))(*groups), len(groups)
+
+
+def _tensors_step(t: _Tensors, groups, grad_scale, skip, stream):
+    t.check_device()
+    hp, count = _groups(groups)
+    dev = grad_scale if isinstance(grad_scale, torch.Tensor) else None
+    here = _here()
+    _check(lib().zero_adam_tensors_step(
+        t.array, t.count, t.grad_dtype, t.out_dtype, hp, count, 1.0 if dev is not None else float(grad_scale),
+        _vec(dev, 1, "grad_scale", torch.float32, here), _vec(skip, 1, "skip", torch.int32, here),
+        _stream_on(stream, here)), "zero_adam_tensors_step")
+
+
+def zero_adam_tensors_step(tensors, groups, grad_scale=1.0, skip=None, stream=None):
+    """One Adam/AdamW step of every tensor of ``tensors`` (of adam_tensor). ``groups``: the hyper-parameters
+    of each group (adam_hparams), or one; ``grad_scale``: a number, or a float32 device tensor of one element."""
+    _tensors_step(_Tensors(tensors), groups, grad_scale, skip, stream)
+
+
+def zero_adam_tensors_step_dev_t(tensors, grad_scale, table, step, status, wd_mode="adamw", skip=None, stream=None):
+    """The step with its counter, grad scale and constants on the device: ``table`` a (groups, len, 9) float32
+    device tensor (adam_table's of each group, stacked), ``step`` int64, ``status`` int32 and ``grad_scale``
+    float32 device tensors of one element. As zero_adam_shard_step_dev_t."""
+    t = tensors if isinstance(tensors, _Tensors) else _Tensors(tensors)
+    t.check_device()
+    here, f32 = _here(), torch.float32
+    mode = {"adamw": ZERO_ADAMW, "l2": ZERO_ADAM_L2}.get(wd_mode, wd_mode)
+    if not isinstance(table, torch.Tensor) or table.dim() != 3 or table.shape[2] != 9:
+        raise ValueError("table must be a (groups, len, 9) float32 device tensor")
+    _check(lib().zero_adam_tensors_step_dev_t(
+        t.array, t.count, t.grad_dtype, t.out_dtype, _vec(grad_scale, 1, "grad_scale", f32, here),
+        _vec(table, table.numel(), "table", f32, here), table.shape[0], table.shape[1],
+        _vec(step, 1, "step", torch.int64, here), _vec(status, 1, "status", torch.int32, here), int(mode),
+        _vec(skip, 1, "skip", torch.int32, here), _stream_on(stream, here)), "zero_adam_tensors_step_dev_t")
+
+
+class AdamTensorsStep:
+    """zero_adam_tensors_step with its tensors marshalled once; a call passes the hyper-parameters of each
+    group and the grad scale. The tensors stay in place while it is used."""
+
+    def __init__(self, tensors, skip=None):
+        self._tensors, self._skip = _Tensors(tensors), skip
+
+    def __call__(self, groups, grad_scale=1.0, stream=None):
+        _tensors_step(self._tensors, groups, grad_scale, self._skip, stream)
+
+    def dev_t(self, grad_scale, table, step, status, wd_mode="adamw", stream=None):
+        """zero_adam_tensors_step_dev_t on the same tensors."""
+        zero_adam_tensors_step_dev_t(self._tensors, grad_scale, table, step, status, wd_mode, self._skip, stream)
+
+
+def _state_moment(codes) -> int:
+    kinds = {torch.int8: 1, torch.uint8: 2}
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in kinds:
+        raise TypeError("codes: int8 (first moment) or uint8 (second moment)")
+    return kinds[codes.dtype]
+
+
+def zero_adam_state_values(codes, scale, values, stream=None):
+    """values = the numbers that an 8-bit moment stands for: ``codes`` int8 (m) or uint8 (v), ``scale`` float32 of
+    one element for each 256, ``values`` float32 of as many elements as ``codes``."""
+    moment, here, n = _state_moment(codes), _here(), codes.numel()
+    _check(lib().zero_adam_state_values(
+        _vec(codes, n, "codes", codes.dtype, here), _vec(scale, -(-n // ZERO_STATE8_BLOCK), "scale", torch.float32, here),
+        n, moment, _vec(values, n, "values", torch.float32, here), _stream_on(stream, here)), "zero_adam_state_values")
+
+
+def zero_adam_state_codes(values, codes, scale, stream=None):
+    """codes, scale = the 8-bit moment of ``values``."""
+    moment, here, n = _state_moment(codes), _here(), codes.numel()
+    _check(lib().zero_adam_state_codes(
+        _vec(values, n, "values", torch.float32, here), n, moment, _vec(codes, n, "codes", codes.dtype, here),
+        _vec(scale, -(-n // ZERO_STATE8_BLOCK), "scale", torch.float32, here), _stream_on(stream, here)),
+        "zero_adam_state_codes")
 
 
 # ------------------------------------------------------------------------------ host (offload) calls

@@ -8,6 +8,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "zero_adam.h"
 #include "zero_internal.h"
 #include "zero_step.h"
 
@@ -428,6 +429,18 @@ zero_status adam_step_host_t(const char* fn, const zero_grad_src* src, uint64_t 
 
 }  // namespace
 
+namespace zero {
+namespace step {
+
+hipError_t advance_step(int64_t* d_step, const int32_t* d_skip, int32_t* d_status, uint32_t table_len,
+                        hipStream_t stream) {
+  hipLaunchKernelGGL(k_step_advance, dim3(1), dim3(64), 0, stream, d_step, d_skip, d_status, table_len);
+  return hipPeekAtLastError();
+}
+
+}  // namespace step
+}  // namespace zero
+
 extern "C" {
 
 zero_status zero_adam_shard_step(const zero_grad_src* src, uint64_t n, float grad_scale,
@@ -484,8 +497,7 @@ zero_status zero_adam_shard_step_dev_t(const zero_grad_src* src, uint64_t n,
                                  out_param, out_dtype, d_skip, stream);
   if (s != ZERO_OK) return s;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(k_step_advance, dim3(1), dim3(64), 0, static_cast<hipStream_t>(stream), d_step,
-                     d_skip, d_status, table_len);
+  (void)zero::step::advance_step(d_step, d_skip, d_status, table_len, static_cast<hipStream_t>(stream));
   return launched(fn);
 }
 
