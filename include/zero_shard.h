@@ -607,6 +607,103 @@ zero_status zero_distill_backward(const zero_distill_in* in, const float* stats,
 zero_status zero_distill_step(const zero_distill_in* in, const float* upstream, float scale,
                               float* loss, void* dlogits, uint64_t ld_dlogits, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Losses over the tokens of a batch, from a model's logits: the log probability of each row's token, the
+ * clipped policy loss with a KL term, and the preference loss of paired answers. With z a row's logits, y
+ * its token and T the temperature,
+ *   l = log softmax(z/T)[y];   dl/dz_v = (1[v = y] - q_v)/T,  q = softmax(z/T)
+ * A row whose token lies outside [0, vocab) (use -1 for prompt and padding) has no token: it is not
+ * read, its l, loss and gradient are 0. A row with a NaN, a +inf or nothing but -inf has no softmax: its
+ * l, loss and gradient are NaN. Exponentials are fp32, each lane's sum too; sums over lanes, l and what is
+ * compared with the clip are fp64, in a fixed order. */
+
+#define ZERO_TOKEN_STATS 8 /* floats that a row keeps for its backward */
+
+typedef struct {
+  uint64_t rows, vocab;
+  int32_t logit_dtype;  /* zero_dtype of logits and of their gradient */
+  int32_t label_bytes;  /* 4 (int32) or 8 (int64) */
+  float temperature;    /* T, 2^-20 to 2^20 */
+  int32_t reserved;
+  const void* logits;   /* [rows, vocab], leading dimension ld_logits */
+  uint64_t ld_logits;
+  const void* label;    /* [rows]: each row's token */
+} zero_token_in;
+
+/* logp[r] = l of each row, e.g. of the policy before its update or of a reference model. stats (device
+ * float[rows*ZERO_TOKEN_STATS], nullable): for zero_token_backward, whose loss is then l itself.
+ * rows == 0 enqueues nothing. Errors: NULLs, vocab 0, label_bytes not 4 or 8, T out of its range, a
+ * leading dimension below the columns, an array off its element size, an output overlapping any array of
+ * the call -> ZERO_E_INVAL; an unknown dtype -> ZERO_E_UNSUPPORTED; rows or vocab above 2^31 - 1 or a byte
+ * count >= 2^63 -> ZERO_E_OVERFLOW. */
+zero_status zero_token_logp(const zero_token_in* in, float* logp, float* stats, void* stream);
+
+/* The policy's terms, device float[rows] each. */
+typedef struct {
+  const float* old_logp;  /* l under the policy that sampled the token */
+  const float* advantage; /* A */
+  const float* ref_logp;  /* l under the reference policy, or NULL (no KL term) */
+  const float* weight;    /* or NULL (1): a row of weight 0 is not read */
+  float clip_low, clip_high; /* the ratio's range is [1 - clip_low, 1 + clip_high]; clip_low in [0, 1], clip_high >= 0 */
+  float kl_coef;          /* >= 0; with 0 ref_logp is not read */
+  int32_t reserved;
+} zero_policy;
+
+/* The clipped policy loss of each row, r = exp(l - old_logp), d = ref_logp - l:
+ *   loss = weight * ( -min(r*A, clamp(r, 1 - clip_low, 1 + clip_high)*A) + kl_coef*(exp(d) - 1 - d) )
+ * with the derivative -A*r in l where r*A is the lesser or equal of the two, else 0, and kl_coef*(1 - exp(d)). A = 0
+ * has no first term, whatever r. loss: device float[rows]. logp: device float[rows] or NULL, l as
+ * zero_token_logp gives it (0 for a row of weight 0). stats: for zero_token_backward.
+ * Errors: as zero_token_logp; NULL old_logp, advantage, loss or stats, clips or kl_coef not finite or
+ * out of range -> ZERO_E_INVAL. */
+zero_status zero_policy_forward(const zero_token_in* in, const zero_policy* p, float* loss, float* logp,
+                                float* stats, void* stream);
+
+/* zero_policy_forward and zero_token_backward in one pass over the logits, for a step that knows its scale
+ * beforehand. upstream: device float[rows] or NULL. Errors and aliasing: as theirs. */
+zero_status zero_policy_step(const zero_token_in* in, const zero_policy* p, const float* upstream,
+                             float scale, float* loss, float* logp, void* dlogits, uint64_t ld_dlogits,
+                             void* stream);
+
+/* Pairs of answers: sequence i is the rows [seq_start[i], seq_start[i+1]), 2p the preferred and 2p+1 the
+ * other answer of pair p. The starts must not descend; they are clamped to [0, rows], and rows in no sequence
+ * have gradient 0. */
+typedef struct {
+  uint64_t pairs;
+  const void* seq_start; /* device int32 or int64 [2*pairs + 1] */
+  int32_t start_bytes;   /* 4 or 8 */
+  int32_t average;       /* 0: a sequence's l is the sum over its tokens; else their mean */
+  const float* ref_logp; /* device float[2*pairs], the sequences' l under the reference, or NULL (0) */
+  const float* weight;   /* device float[pairs] or NULL (1) */
+  float beta;            /* finite */
+  float label_smoothing; /* e, 0 to 1 */
+  float margin;          /* finite */
+  int32_t reserved;
+} zero_preference;
+
+/* The preference loss of each pair, with L the sequences' l less the reference's:
+ *   x = beta*(L[2p] - L[2p+1]) - margin
+ *   loss = weight * ( (1 - e)*log(1 + exp(-x)) + e*log(1 + exp(x)) )
+ * A sequence without a token has l = 0; a pair of weight 0 has loss and gradient 0. loss: device
+ * float[pairs]; logp (nullable): device float[rows], each row's l; seq_logp (nullable): device
+ * float[2*pairs], the sequences' l (the reference not taken off). stats: for zero_token_backward, whose
+ * upstream is one number for each pair. pairs == 0 leaves the rows' l alone; rows == 0 the pairs' losses.
+ * Errors: as zero_token_logp; NULLs, start_bytes not 4 or 8, a beta, smoothing or margin out of range ->
+ * ZERO_E_INVAL; pairs above 2^23 -> ZERO_E_OVERFLOW. */
+zero_status zero_preference_forward(const zero_token_in* in, const zero_preference* p, float* loss,
+                                    float* logp, float* seq_logp, float* stats, void* stream);
+
+/* The gradient in the logits from the stats that a forward over the same inputs left:
+ *   dlogits[r, v] = scale * upstream[k] * dloss[k]/dl[r] * (1[v = y_r] - q_v)/T
+ * k is the row, or the row's pair after zero_preference_forward; upstream (device float[n_upstream],
+ * nullable: 1) must cover them (a k past it gives NaN). dlogits [rows, vocab] of logit_dtype, leading dimension ld_dlogits; it may
+ * be the logits themselves (same pointer and leading dimension), and otherwise overlaps nothing of the
+ * call. A row whose derivative is 0 is not read. Errors: as zero_token_logp; scale not finite ->
+ * ZERO_E_INVAL. */
+zero_status zero_token_backward(const zero_token_in* in, const float* stats, const float* upstream,
+                                uint64_t n_upstream, float scale, void* dlogits, uint64_t ld_dlogits,
+                                void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* zero_status_str(zero_status s);
 

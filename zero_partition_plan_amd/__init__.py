@@ -37,6 +37,8 @@ __all__ = [
     "ZERO_ACT_SILU", "zero_linear_workspace_bytes", "zero_linear_forward", "zero_linear_backward",
     "ZeroDistillIn", "ZERO_DISTILL_MAX_TOPK", "ZERO_DISTILL_MAX_VOCAB", "zero_distill_forward",
     "zero_distill_backward", "zero_distill_step",
+    "ZeroTokenIn", "ZeroPolicy", "ZeroPreference", "ZERO_TOKEN_STATS", "zero_token_logp", "zero_policy_forward",
+    "zero_policy_step", "zero_preference_forward", "zero_token_backward",
     "zero_status_str", "zero_last_error",
 ]
 
@@ -53,6 +55,7 @@ ZERO_STATIC_SQ_PARTIALS = 4 << 20
 ZERO_STATIC_MAX_ELEMS = (ZERO_STATIC_SQ_PARTIALS - 1024) * 256
 
 ZERO_STATE8_BLOCK = 256
+ZERO_TOKEN_STATS = 8
 ZERO_ADAM_MAX_TENSORS = 65536
 ZERO_ADAM_MAX_GROUPS = 16
 
@@ -127,6 +130,23 @@ class ZeroDistillIn(ctypes.Structure):
                 ("ld_top", ctypes.c_uint64), ("tail", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
 
 
+class ZeroTokenIn(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("logit_dtype", ctypes.c_int32),
+                ("label_bytes", ctypes.c_int32), ("temperature", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_uint64), ("label", ctypes.c_void_p)]
+
+
+class ZeroPolicy(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("old_logp", "advantage", "ref_logp", "weight")] + [
+        (k, ctypes.c_float) for k in ("clip_low", "clip_high", "kl_coef")] + [("reserved", ctypes.c_int32)]
+
+
+class ZeroPreference(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_uint64), ("seq_start", ctypes.c_void_p), ("start_bytes", ctypes.c_int32),
+                ("average", ctypes.c_int32), ("ref_logp", ctypes.c_void_p), ("weight", ctypes.c_void_p)] + [
+        (k, ctypes.c_float) for k in ("beta", "label_smoothing", "margin")] + [("reserved", ctypes.c_int32)]
+
+
 def adam_hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, wd_mode="adamw",
                  step=1) -> ZeroAdamHParams:
     mode = {"adamw": ZERO_ADAMW, "l2": ZERO_ADAM_L2}.get(wd_mode, wd_mode)
@@ -190,6 +210,11 @@ def lib() -> ctypes.CDLL:
             "zero_distill_forward": [P(ZeroDistillIn), vp, vp, vp],
             "zero_distill_backward": [P(ZeroDistillIn), vp, vp, ctypes.c_float, vp, u64, vp],
             "zero_distill_step": [P(ZeroDistillIn), vp, ctypes.c_float, vp, vp, u64, vp],
+            "zero_token_logp": [P(ZeroTokenIn), vp, vp, vp],
+            "zero_policy_forward": [P(ZeroTokenIn), P(ZeroPolicy), vp, vp, vp, vp],
+            "zero_policy_step": [P(ZeroTokenIn), P(ZeroPolicy), vp, ctypes.c_float, vp, vp, vp, u64, vp],
+            "zero_preference_forward": [P(ZeroTokenIn), P(ZeroPreference), vp, vp, vp, vp, vp],
+            "zero_token_backward": [P(ZeroTokenIn), vp, vp, u64, ctypes.c_float, vp, u64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -897,6 +922,102 @@ def zero_adam_state_codes(values, codes, scale, stream=None):
         _vec(values, n, "values", torch.float32, here), n, moment, _vec(codes, n, "codes", codes.dtype, here),
         _vec(scale, -(-n // ZERO_STATE8_BLOCK), "scale", torch.float32, here), _stream_on(stream, here)),
         "zero_adam_state_codes")
+
+
+# ------------------------------------------------------------------------------ losses over tokens
+
+def _token_in(logits, label, temperature, here: int) -> ZeroTokenIn:
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or not isinstance(label, torch.Tensor):
+        raise TypeError("logits must be a 2-D and label a 1-D device tensor")
+    if logits.dtype not in _TORCH_DT:
+        raise TypeError("logits must be float32, float16 or bfloat16")
+    if label.dtype is not torch.int64 and label.dtype is not torch.int32:
+        raise TypeError("label must be int32 or int64")
+    R, V = logits.shape
+    lp, ld = _mat(logits, R, V, "logits", logits.dtype, here)
+    return ZeroTokenIn(R, V, _TORCH_DT[logits.dtype], label.element_size(), float(temperature), 0, lp, ld,
+                       _vec(label, R, "label", label.dtype, here))
+
+
+def _policy(rows, old_logp, advantage, ref_logp, weight, clip, kl_coef, here: int) -> ZeroPolicy:
+    f32 = torch.float32
+    low, high = clip if isinstance(clip, (tuple, list)) else (clip, clip)
+    return ZeroPolicy(_vec(old_logp, rows, "old_logp", f32, here), _vec(advantage, rows, "advantage", f32, here),
+                      _vec(ref_logp, rows, "ref_logp", f32, here), _vec(weight, rows, "weight", f32, here),
+                      float(low), float(high), float(kl_coef), 0)
+
+
+def zero_token_logp(logits, label, logp, temperature: float = 1.0, stats=None, stream=None):
+    """logp[r] = the log probability of row r's token under softmax(logits / temperature) (0 where label is -1).
+    ``logits`` (rows, vocab), ``label`` int32 or int64 (rows,), ``logp`` float32 (rows,); ``stats``: float32
+    (rows, ZERO_TOKEN_STATS), kept for zero_token_backward, or None."""
+    here, f32 = _here(), torch.float32
+    a = _token_in(logits, label, temperature, here)
+    _check(lib().zero_token_logp(ctypes.byref(a), _vec(logp, a.rows, "logp", f32, here),
+                                 _vec(stats, ZERO_TOKEN_STATS * a.rows, "stats", f32, here), _stream_on(stream, here)),
+           "zero_token_logp")
+
+
+def zero_policy_forward(logits, label, old_logp, advantage, loss, stats, ref_logp=None, weight=None, clip=0.2,
+                        kl_coef: float = 0.0, temperature: float = 1.0, logp=None, stream=None):
+    """loss[r] = weight[r] * (the clipped policy loss of row r's token + kl_coef * its KL estimate). float32
+    (rows,) tensors but for ``logits``, ``label`` and ``stats`` (as zero_token_logp); ``clip``: one width or (low, high)."""
+    here, f32 = _here(), torch.float32
+    a = _token_in(logits, label, temperature, here)
+    p = _policy(a.rows, old_logp, advantage, ref_logp, weight, clip, kl_coef, here)
+    _check(lib().zero_policy_forward(
+        ctypes.byref(a), ctypes.byref(p), _vec(loss, a.rows, "loss", f32, here), _vec(logp, a.rows, "logp", f32, here),
+        _vec(stats, ZERO_TOKEN_STATS * a.rows, "stats", f32, here), _stream_on(stream, here)), "zero_policy_forward")
+
+
+def zero_policy_step(logits, label, old_logp, advantage, loss, dlogits, ref_logp=None, weight=None, clip=0.2,
+                     kl_coef: float = 0.0, temperature: float = 1.0, logp=None, upstream=None, scale: float = 1.0,
+                     stream=None):
+    """zero_policy_forward and zero_token_backward in one pass over the logits; ``dlogits`` may be ``logits``."""
+    here, f32 = _here(), torch.float32
+    a = _token_in(logits, label, temperature, here)
+    p = _policy(a.rows, old_logp, advantage, ref_logp, weight, clip, kl_coef, here)
+    _check(lib().zero_policy_step(
+        ctypes.byref(a), ctypes.byref(p), _vec(upstream, a.rows, "upstream", f32, here), float(scale),
+        _vec(loss, a.rows, "loss", f32, here), _vec(logp, a.rows, "logp", f32, here),
+        *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype, here), _stream_on(stream, here)), "zero_policy_step")
+
+
+def zero_preference_forward(logits, label, seq_start, loss, stats, ref_logp=None, weight=None, beta: float = 0.1,
+                            label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                            temperature: float = 1.0, logp=None, seq_logp=None, stream=None):
+    """loss[p] = weight[p] * the preference loss of pair p, whose answers are the rows seq_start[2p] to seq_start[2p+1]
+    (preferred) and from there to seq_start[2p+2]. ``seq_start``: int32 or int64 (2 * pairs + 1,); ``loss`` and
+    ``weight`` float32 (pairs,); ``ref_logp`` and ``seq_logp`` float32 (2 * pairs,); ``logp`` float32 (rows,);
+    ``stats`` as zero_token_logp."""
+    here, f32 = _here(), torch.float32
+    a = _token_in(logits, label, temperature, here)
+    if not isinstance(seq_start, torch.Tensor) or seq_start.dtype not in (torch.int32, torch.int64):
+        raise TypeError("seq_start must be an int32 or int64 device tensor")
+    n = seq_start.numel()
+    if n % 2 != 1:
+        raise ValueError("seq_start holds 2 * pairs + 1 rows")
+    pairs = n // 2
+    p = ZeroPreference(pairs, _vec(seq_start, n, "seq_start", seq_start.dtype, here), seq_start.element_size(),
+                       int(bool(average)), _vec(ref_logp, 2 * pairs, "ref_logp", f32, here),
+                       _vec(weight, pairs, "weight", f32, here), float(beta), float(label_smoothing), float(margin), 0)
+    _check(lib().zero_preference_forward(
+        ctypes.byref(a), ctypes.byref(p), _vec(loss, pairs, "loss", f32, here), _vec(logp, a.rows, "logp", f32, here),
+        _vec(seq_logp, 2 * pairs, "seq_logp", f32, here), _vec(stats, ZERO_TOKEN_STATS * a.rows, "stats", f32, here),
+        _stream_on(stream, here)), "zero_preference_forward")
+
+
+def zero_token_backward(logits, label, stats, dlogits, upstream=None, scale: float = 1.0, temperature: float = 1.0,
+                        stream=None):
+    """dlogits = scale * upstream * the gradient of the loss whose forward left ``stats``; ``upstream``: float32 (rows,),
+    after zero_preference_forward (pairs,), or None; ``dlogits`` may be ``logits`` itself."""
+    here, f32 = _here(), torch.float32
+    a = _token_in(logits, label, temperature, here)
+    n = upstream.numel() if isinstance(upstream, torch.Tensor) else 0
+    _check(lib().zero_token_backward(
+        ctypes.byref(a), _vec(stats, ZERO_TOKEN_STATS * a.rows, "stats", f32, here),
+        _vec(upstream, n, "upstream", f32, here), n, float(scale),
+        *_mat(dlogits, a.rows, a.vocab, "dlogits", logits.dtype, here), _stream_on(stream, here)), "zero_token_backward")
 
 
 # ------------------------------------------------------------------------------ host (offload) calls

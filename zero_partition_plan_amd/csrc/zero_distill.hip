@@ -20,13 +20,13 @@
 #include <stdint.h>
 
 #include "zero_internal.h"
+#include "zero_rows.h"
 
 namespace zero {
 namespace {
 
 constexpr uint64_t kMaxSize = 0x7fffffffu;
 constexpr uint64_t kGridRows = 1u << 21;
-constexpr float kLowest = -3.402823466e38f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct Args {
@@ -67,37 +67,11 @@ struct MaxSum {
   float m, s;
 };
 
-// 2^x for x <= 0: the instruction itself (about one unit in the last place, 0 below 2^-126)
-__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
-
 __device__ __forceinline__ MaxSum join(const Args& a, MaxSum x, MaxSum y) {
   MaxSum r;
   r.m = x.m > y.m ? x.m : y.m;
   r.s = x.s * ex2(mul_c(a, x.m - r.m)) + y.s * ex2(mul_c(a, y.m - r.m));
   return r;
-}
-
-// Reductions over a wave in a fixed order, by lane moves inside the vector unit: a row's latency is a
-// chain of them, and a move through LDS takes several times as long. The result is in every lane.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float moved(float v, float none) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
-                                                               __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
-}
-
-template <typename Op>
-__device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
-  v = op(v, moved<0x111, 0xf>(v, none));  // lanes 1, 2, 4, 8 before, in rows of 16
-  v = op(v, moved<0x112, 0xf>(v, none));
-  v = op(v, moved<0x114, 0xf>(v, none));
-  v = op(v, moved<0x118, 0xf>(v, none));
-  v = op(v, moved<0x142, 0xa>(v, none));  // a row's last lane to the next row
-  v = op(v, moved<0x143, 0xc>(v, none));  // lane 31 to the upper rows
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  return wave_reduce(v, 0.0f, [](float x, float y) { return x + y; });
 }
 
 // the larger, or a NaN if there is one
@@ -113,14 +87,6 @@ __device__ __forceinline__ float load_as_float(const void* p, int32_t dtype, uin
   if (dtype == ZERO_F16) return (float)static_cast<const _Float16*>(p)[i];
   return (float)static_cast<const __bf16*>(p)[i];
 }
-
-// 16 bytes of logits at any element offset.
-template <typename T>
-struct Pack {
-  static constexpr int n = 16 / sizeof(T);
-  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-  typedef vec type;
-};
 
 // What the first wave leaves for the others.
 struct Teacher {
