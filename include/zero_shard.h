@@ -549,6 +549,81 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
                                  void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
                                  void* workspace, uint64_t workspace_bytes, void* stream);
 
+/* Block boundaries on a residual stream: the norm of a block's output, its gate and scale, the sum
+ * with the stream, and the norm that the next block reads, in one pass; and their gradients. Per row,
+ * with n = features, `branch` the block's output and x the stream before it:
+ *   norm(v) = (v - mean) * rstd * weight + bias
+ *     ZERO_NORM_LAYER: mean = sum(v)/n, rstd = 1/sqrt(sum((v - mean)^2)/n + eps)
+ *     ZERO_NORM_RMS:   mean = 0, rstd = 1/sqrt(sum(v^2)/n + eps);   ZERO_NORM_NONE: norm(v) = v
+ *   y = round(residual_scale*x + branch_scale*gate*norm_post(branch))      the stream's type
+ *   h = round16(norm_pre(y))                                                of y as it is stored
+ * Sums are fp32 in a fixed order; nothing between is rounded to 16 bits. A row whose squares leave fp32 has
+ * rstd 0, one of zeros with eps 0 is NaN. */
+
+typedef enum { ZERO_NORM_NONE = 0, ZERO_NORM_RMS = 1, ZERO_NORM_LAYER = 2 } zero_norm;
+
+#define ZERO_NORM_MAX_FEATURES 16384
+
+typedef struct {
+  uint64_t rows, features;
+  uint64_t gate_rows;    /* consecutive rows that share a row of gate, >= 1: 1 for a gate of each token, a
+                            sequence's length for one of each sequence, `rows` for one row for all */
+  int32_t dtype;         /* ZERO_BF16 or ZERO_F16: branch, gate, h, parameters */
+  int32_t stream_dtype;  /* dtype or ZERO_F32: x, y and their gradients */
+  int32_t post, pre;     /* zero_norm of the branch, and of the next block's input */
+  float eps;             /* >= 0, both norms */
+  float residual_scale, branch_scale;
+  int32_t reserved;
+  const void* branch;    /* [rows, n], or NULL: no block, y = x (post ZERO_NORM_NONE, no gate, scales not read) */
+  uint64_t ld_branch;
+  const void* gate;      /* [ceil(rows/gate_rows), n] or NULL (1) */
+  uint64_t ld_gate;
+  const void *post_weight, *post_bias; /* [n] or NULL (1, 0); a norm of ZERO_NORM_NONE has none */
+  const void *pre_weight, *pre_bias;
+} zero_norm_block;
+
+/* y and h of every row. x [rows, n] and y [rows, n] of stream_dtype; y is not written without a branch (may be
+ * NULL). h [rows, n] of dtype, required unless pre is ZERO_NORM_NONE (then not written). stats: device
+ * float[4*rows] or NULL: each row's mean and rstd of the branch, mean and rstd of y (0 and 1 where there is no
+ * norm), for the backward.
+ * rows == 0 or features == 0 enqueues nothing. Aliasing: y may be x itself (same pointer and leading
+ * dimension); otherwise y, h and stats overlap no array of the call. Arrays at any multiple of their element
+ * size; leading dimensions are not looked at for a single row.
+ * Errors: NULLs, nothing to do (no branch and no pre norm), an unknown norm, parameters of no norm, a gate or
+ * post norm without a branch, gate_rows 0 with a gate, eps, scales not finite or eps negative, a leading
+ * dimension below the columns, aliasing, an array off its element size -> ZERO_E_INVAL; dtype ZERO_F32, a
+ * stream_dtype neither dtype nor ZERO_F32, features above ZERO_NORM_MAX_FEATURES -> ZERO_E_UNSUPPORTED; rows
+ * above 2^27 or a byte count >= 2^63 -> ZERO_E_OVERFLOW. */
+zero_status zero_norm_forward(const zero_norm_block* b, const void* x, uint64_t ldx, void* y,
+                              uint64_t ldy, void* h, uint64_t ldh, float* stats, void* stream);
+
+/* Bytes of device workspace that zero_norm_backward of this many rows and features needs, for any types, norms
+ * and outputs (gate_rows as in the block; any value without a gate). Starts on 16 bytes, holds nothing
+ * between calls, needs no clearing, one for each call that may run at the same time. Host only; never
+ * fails (sizes the call refuses give 0). */
+uint64_t zero_norm_workspace_bytes(uint64_t rows, uint64_t features, uint64_t gate_rows);
+
+/* The gradients of zero_norm_forward from dh = dL/dh (of dtype; not read without a pre norm) and dy = dL/dy by
+ * the stream's later uses (of stream_dtype; NULL: 0), with stats and y (not read without a pre norm) of the
+ * forward. With D = dy + the gradient through the pre norm:
+ *   dx = residual_scale*D;  dbranch = through the post norm, branch_scale*gate*D
+ *   dgate = sum over the rows that share it of branch_scale*D*norm_post(branch)
+ *   dpost_weight, dpost_bias, dpre_weight, dpre_bias: sums over all rows
+ * Without a branch D is dx, and y the stream x. dx of stream_dtype, dbranch of dtype; dgate (as gate,
+ * leading dimension ld_dgate) and the parameter gradients (contiguous) of grad_dtype (dtype or ZERO_F32),
+ * written, or with accumulate != 0 added to in fp32 and rounded once. Any subset, one at least; rows ==
+ * 0 zeroes the sums (leaves them with accumulate). Aliasing: dx may be dy itself (same pointer and leading
+ * dimension); otherwise no output or workspace overlaps an array of the call. Errors: as zero_norm_forward; a
+ * gradient of an array the block does not have, missing stats, a missing, short or misaligned workspace ->
+ * ZERO_E_INVAL; grad_dtype neither dtype nor ZERO_F32 -> ZERO_E_UNSUPPORTED. */
+zero_status zero_norm_backward(const zero_norm_block* b, const float* stats, const void* y,
+                               uint64_t ldy, const void* dy, uint64_t lddy, const void* dh,
+                               uint64_t lddh, void* dx, uint64_t lddx, void* dbranch,
+                               uint64_t lddbranch, void* dgate, uint64_t lddgate, void* dpost_weight,
+                               void* dpost_bias, void* dpre_weight, void* dpre_bias,
+                               int32_t grad_dtype, int32_t accumulate, void* workspace,
+                               uint64_t workspace_bytes, void* stream);
+
 #define ZERO_DISTILL_MAX_TOPK 1024     /* teacher entries of one row */
 #define ZERO_DISTILL_MAX_VOCAB 393216  /* logits of one row */
 

@@ -27,6 +27,7 @@ Modules:
              rank sends per step under each stage, and the stage-choice rule  [P1 一/二/三/四; P3 stages]
   layer      a linear layer and the top-logit distillation loss with their gradients, in fp64
              (the passes a gathered layer runs: [P1 三; P2 Stage 3]; arithmetic not on the pages)
+  norm       the norms before and after a block with its gate and scales, in fp64 (not on the pages)
   token      losses over tokens with their gradients, in fp64 (not on the pages)
   state8     Adam's moments in 8 bits, and a step on them (not on the pages)
 
@@ -50,6 +51,7 @@ from .adam import (
 )
 from .gather import gather_range
 from . import layer
+from . import norm
 from . import state8
 from . import token
 from .memory import (MemoryEstimation, estimate_memory_per_gpu, stage_bytes_exact, stage_comm_bytes, STAGES,
@@ -60,7 +62,7 @@ __all__ = [
     "cast_bf16_rne", "cast_fp16_rne", "widen_bf16", "widen_fp16",
     "AdamHParams", "AdamScalars", "adam_scalars", "adam_update", "replica_sum",
     "nonfinite_flag", "shard_sqnorm", "clip_coefficient", "sharded_step", "unsharded_step",
-    "gather_range", "layer", "state8", "token",
+    "gather_range", "layer", "norm", "state8", "token",
     "MemoryEstimation", "estimate_memory_per_gpu", "stage_bytes_exact", "stage_comm_bytes", "STAGES",
     "choose_stage",
 ]

@@ -37,6 +37,8 @@ __all__ = [
     "ZERO_ACT_SILU", "zero_linear_workspace_bytes", "zero_linear_forward", "zero_linear_backward",
     "ZeroDistillIn", "ZERO_DISTILL_MAX_TOPK", "ZERO_DISTILL_MAX_VOCAB", "zero_distill_forward",
     "zero_distill_backward", "zero_distill_step",
+    "ZeroNormBlock", "ZERO_NORM_NONE", "ZERO_NORM_RMS", "ZERO_NORM_LAYER", "ZERO_NORM_MAX_FEATURES",
+    "zero_norm_forward", "zero_norm_backward", "zero_norm_workspace_bytes",
     "ZeroTokenIn", "ZeroPolicy", "ZeroPreference", "ZERO_TOKEN_STATS", "zero_token_logp", "zero_policy_forward",
     "zero_policy_step", "zero_preference_forward", "zero_token_backward",
     "zero_status_str", "zero_last_error",
@@ -54,6 +56,8 @@ ZERO_DISTILL_MAX_VOCAB = 393216
 ZERO_STATIC_SQ_PARTIALS = 4 << 20
 ZERO_STATIC_MAX_ELEMS = (ZERO_STATIC_SQ_PARTIALS - 1024) * 256
 
+ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_NORM_LAYER = range(3)
+ZERO_NORM_MAX_FEATURES = 16384
 ZERO_STATE8_BLOCK = 256
 ZERO_TOKEN_STATS = 8
 ZERO_ADAM_MAX_TENSORS = 65536
@@ -128,6 +132,15 @@ class ZeroDistillIn(ctypes.Structure):
                 ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_uint64),
                 ("top_index", ctypes.c_void_p), ("top_logits", ctypes.c_void_p),
                 ("ld_top", ctypes.c_uint64), ("tail", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
+
+
+class ZeroNormBlock(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_uint64) for k in ("rows", "features", "gate_rows")] + [
+        (k, ctypes.c_int32) for k in ("dtype", "stream_dtype", "post", "pre")] + [
+        (k, ctypes.c_float) for k in ("eps", "residual_scale", "branch_scale")] + [
+        ("reserved", ctypes.c_int32), ("branch", ctypes.c_void_p), ("ld_branch", ctypes.c_uint64),
+        ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_uint64)] + [
+        (k, ctypes.c_void_p) for k in ("post_weight", "post_bias", "pre_weight", "pre_bias")]
 
 
 class ZeroTokenIn(ctypes.Structure):
@@ -210,6 +223,9 @@ def lib() -> ctypes.CDLL:
             "zero_distill_forward": [P(ZeroDistillIn), vp, vp, vp],
             "zero_distill_backward": [P(ZeroDistillIn), vp, vp, ctypes.c_float, vp, u64, vp],
             "zero_distill_step": [P(ZeroDistillIn), vp, ctypes.c_float, vp, vp, u64, vp],
+            "zero_norm_forward": [P(ZeroNormBlock), vp, u64, vp, u64, vp, u64, vp, vp],
+            "zero_norm_backward": [P(ZeroNormBlock), vp, vp, u64, vp, u64, vp, u64, vp, u64, vp, u64, vp, u64,
+                                   vp, vp, vp, vp, i32, i32, vp, u64, vp],
             "zero_token_logp": [P(ZeroTokenIn), vp, vp, vp],
             "zero_policy_forward": [P(ZeroTokenIn), P(ZeroPolicy), vp, vp, vp, vp],
             "zero_policy_step": [P(ZeroTokenIn), P(ZeroPolicy), vp, ctypes.c_float, vp, vp, vp, u64, vp],
@@ -224,6 +240,8 @@ def lib() -> ctypes.CDLL:
         L.zero_sq_partials_len.restype = u64
         L.zero_linear_workspace_bytes.argtypes = [u64, u64, u64, i32]
         L.zero_linear_workspace_bytes.restype = u64
+        L.zero_norm_workspace_bytes.argtypes = [u64, u64, u64]
+        L.zero_norm_workspace_bytes.restype = u64
         L.zero_status_str.argtypes = [ctypes.c_int]
         L.zero_status_str.restype = ctypes.c_char_p
         L.zero_last_error.argtypes = []
@@ -922,6 +940,97 @@ def zero_adam_state_codes(values, codes, scale, stream=None):
         _vec(values, n, "values", torch.float32, here), n, moment, _vec(codes, n, "codes", codes.dtype, here),
         _vec(scale, -(-n // ZERO_STATE8_BLOCK), "scale", torch.float32, here), _stream_on(stream, here)),
         "zero_adam_state_codes")
+
+
+# ------------------------------------------------------------------------------ block boundaries
+
+_NORMS = {"none": ZERO_NORM_NONE, "rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
+
+
+def _norm_block(stream_like, what, dtype, branch, gate, gate_rows, post, post_weight, post_bias, pre, pre_weight, pre_bias,
+                eps, residual_scale, branch_scale, here: int) -> ZeroNormBlock:
+    """The block of a stream tensor (rows, features); ``dtype``: the block's 16-bit type."""
+    if not isinstance(stream_like, torch.Tensor) or stream_like.dim() != 2:
+        raise TypeError(f"{what} must be a 2-D device tensor")
+    R, d = stream_like.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError("the block's tensors must be bfloat16 or float16")
+    if stream_like.dtype is not dtype and stream_like.dtype is not torch.float32:
+        raise TypeError(f"{what}: {dtype} or float32 expected")
+    kinds = []
+    for k in (post, pre):
+        kind = _NORMS.get(k, k)
+        if not isinstance(kind, int):
+            raise ValueError(f"unknown norm {k!r}: one of {', '.join(_NORMS)}")
+        kinds.append(kind)
+    if gate is not None and int(gate_rows) < 1:
+        raise ValueError("gate_rows must be at least 1")
+    per = int(gate_rows)
+    bp, ldb = _mat(branch, R, d, "branch", dtype, here)
+    gp, ldg = _mat(gate, -(-R // per), d, "gate", dtype, here) if gate is not None else (None, d)
+    return ZeroNormBlock(R, d, max(per, 0), _TORCH_DT[dtype], _TORCH_DT[stream_like.dtype], *kinds, float(eps),
+                         float(residual_scale), float(branch_scale), 0, bp, ldb, gp, ldg,
+                         _vec(post_weight, d, "post_weight", dtype, here), _vec(post_bias, d, "post_bias", dtype, here),
+                         _vec(pre_weight, d, "pre_weight", dtype, here), _vec(pre_bias, d, "pre_bias", dtype, here))
+
+
+def _dtype_of(*tensors):
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            return t.dtype
+    return None
+
+
+def zero_norm_workspace_bytes(rows: int, features: int, gate_rows: int = 1) -> int:
+    """Bytes of device workspace that zero_norm_backward of this size needs."""
+    return int(lib().zero_norm_workspace_bytes(rows, features, gate_rows))
+
+
+def zero_norm_forward(x, h=None, branch=None, y=None, gate=None, gate_rows: int = 1, post="none", post_weight=None,
+                      post_bias=None, pre="rms", pre_weight=None, pre_bias=None, eps: float = 1e-5,
+                      residual_scale: float = 1.0, branch_scale: float = 1.0, stats=None, stream=None):
+    """y = residual_scale * x + branch_scale * gate * post_norm(branch) and h = pre_norm(y), in one pass. ``x`` and ``y``
+    (rows, features) of the stream's type (the block's or float32; y may be x), ``branch``, ``h``, ``gate`` and the
+    parameters bfloat16 or float16; ``gate`` has a row for every ``gate_rows`` rows (rows: one row for all). Without
+    a branch y is x itself. Norms: "none", "rms", "layer". ``stats``: float32 (rows, 4), kept for the backward."""
+    here, f32 = _here(), torch.float32
+    dt = _dtype_of(branch, h)
+    b = _norm_block(x, "x", dt, branch, gate, gate_rows, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
+                    residual_scale, branch_scale, here)
+    R, d = x.shape
+    _check(lib().zero_norm_forward(
+        ctypes.byref(b), *_mat(x, R, d, "x", x.dtype, here), *_mat(y, R, d, "y", x.dtype, here),
+        *_mat(h, R, d, "h", dt, here), _vec(stats, 4 * R, "stats", f32, here), _stream_on(stream, here)),
+        "zero_norm_forward")
+
+
+def zero_norm_backward(y, stats, dy=None, dh=None, branch=None, gate=None, gate_rows: int = 1, post="none",
+                       post_weight=None, post_bias=None, pre="rms", pre_weight=None, pre_bias=None, eps: float = 1e-5,
+                       residual_scale: float = 1.0, branch_scale: float = 1.0, dx=None, dbranch=None, dgate=None,
+                       dpost_weight=None, dpost_bias=None, dpre_weight=None, dpre_bias=None, accumulate: bool = False,
+                       workspace=None, stream=None):
+    """The gradients of zero_norm_forward from ``dh`` and ``dy`` (or None: 0), with its ``y`` (without a branch: x) and
+    ``stats``. ``dx`` of the stream's type (it may be dy), ``dbranch`` of the block's; ``dgate`` and the parameters'
+    gradients of the block's type or float32, added to with ``accumulate``; each optional. ``workspace``: a device
+    tensor of zero_norm_workspace_bytes (read and written only where a parameter's or a shared gate's gradient is
+    asked for). Without a pre norm ``y`` may be None if ``dy`` or ``dx`` is given."""
+    here, f32 = _here(), torch.float32
+    like = y if y is not None else dy if dy is not None else dx
+    dt = _dtype_of(branch, dh, dbranch)
+    b = _norm_block(like, "y", dt, branch, gate, gate_rows, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
+                    residual_scale, branch_scale, here)
+    R, d = like.shape
+    sdt, gates = like.dtype, -(-R // max(1, int(gate_rows)))
+    gdt = _dtype_of(dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias) or dt
+    if gdt not in _TORCH_DT:
+        raise TypeError("dgate and the parameters' gradients: the block's dtype or float32")
+    _check(lib().zero_norm_backward(
+        ctypes.byref(b), _vec(stats, 4 * R, "stats", f32, here), *_mat(y, R, d, "y", sdt, here),
+        *_mat(dy, R, d, "dy", sdt, here), *_mat(dh, R, d, "dh", dt, here), *_mat(dx, R, d, "dx", sdt, here),
+        *_mat(dbranch, R, d, "dbranch", dt, here), *_mat(dgate, gates, d, "dgate", gdt, here),
+        _vec(dpost_weight, d, "dpost_weight", gdt, here), _vec(dpost_bias, d, "dpost_bias", gdt, here),
+        _vec(dpre_weight, d, "dpre_weight", gdt, here), _vec(dpre_bias, d, "dpre_bias", gdt, here), _TORCH_DT[gdt],
+        int(bool(accumulate)), *_workspace(workspace, here), _stream_on(stream, here)), "zero_norm_backward")
 
 
 # ------------------------------------------------------------------------------ losses over tokens

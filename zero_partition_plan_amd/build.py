@@ -27,7 +27,7 @@ SOURCES = [os.path.join(CSRC, "zero_host.cpp"), os.path.join(CSRC, "zero_step.hi
            os.path.join(CSRC, "zero_offload.cpp"), os.path.join(CSRC, "zero_arena.cpp"),
            os.path.join(CSRC, "zero_linear.hip"), os.path.join(CSRC, "zero_gemm.hip"),
            os.path.join(CSRC, "zero_distill.hip"), os.path.join(CSRC, "zero_adam_tensors.hip"),
-           os.path.join(CSRC, "zero_token.hip")]
+           os.path.join(CSRC, "zero_token.hip"), os.path.join(CSRC, "zero_norm.hip")]
 # the step's kernel variants, compiled once per replica / output dtype pair (zero_dtype values:
 # 0 fp32, 1 fp16, 2 bf16; an fp32 "output" means none and also carries the reduce pass)
 STEP_KERNELS = os.path.join(CSRC, "zero_step_kernels.hip")
@@ -37,6 +37,10 @@ STEP_PAIRS = [(r, o) for r in (0, 1, 2) for o in (0, 1, 2)]
 # the linear layer makes: x W^T, dz W, dz^T x
 GEMM_KERNELS = os.path.join(CSRC, "zero_gemm_kernels.hip")
 GEMM_VARIANTS = [(d, a, b) for d in (1, 2) for a, b in ((0, 0), (0, 1), (1, 1))]
+
+# the block norms' row kernels, once per 16-bit type and stream type (1: fp32)
+NORM_KERNELS = os.path.join(CSRC, "zero_norm_kernels.hip")
+NORM_VARIANTS = [(d, s) for d in (1, 2) for s in (0, 1)]
 
 FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -61,6 +65,8 @@ def _units():
               for r, o in STEP_PAIRS]
     units += [(GEMM_KERNELS, [f"ZERO_GEMM_DT={d}", f"ZERO_GEMM_AK={a}", f"ZERO_GEMM_BK={b}"],
                f"zero_gemm_kernels_{d}{a}{b}") for d, a, b in GEMM_VARIANTS]
+    units += [(NORM_KERNELS, [f"ZERO_NORM_DT={d}", f"ZERO_NORM_S32={s}"], f"zero_norm_kernels_{d}{s}")
+              for d, s in NORM_VARIANTS]
     return units
 
 
