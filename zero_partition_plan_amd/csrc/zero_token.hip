@@ -1,14 +1,17 @@
 // Losses over tokens on gfx950: the log probability of each row's token, the clipped policy loss with a KL
 // term, the preference loss of paired answers, and their gradient in the logits.
 //
-// One block per row. In base-2 logarithms with c = log2(e)/T, m the largest logit but the token's and
-// s = sum over v but the token of 2^((z_v - m) c): leaving the token out keeps l = -log1p(s exp((m - z_y)/T)) and
-// 1 - q_y = a/(1 + a) exact for tokens the model is sure of. Each lane's sum is fp32, the join of lanes and
-// everything behind it fp64: the policy's ratio is compared with its clip, where an error in l decides a
-// row's whole gradient. The gradient is F * 2^((z_v - M) c) for every entry, and the token's own over it.
+// One block per row. In base-2 logarithms with c = log2(e)/T, m one of the largest logits and s = sum over v but
+// the token of 2^((z_v - m) c): leaving the token out keeps l = -log1p(s exp((m - z_y)/T)) and 1 - q_y = a/(1 + a) exact
+// for tokens the model is sure of. Each lane's sum is fp32, the join of lanes and everything behind it fp64: the
+// policy's ratio is compared with its clip, where an error in l decides a row's whole gradient. The gradient is
+// F * 2^((z_v - M) c) for every entry, and the token's own over it.
 //
 // Memory is the bound: the loss alone and the gradient alone read the row once, and the policy's step keeps
-// it in registers between the two, as far as it fits; longer rows are read twice.
+// it in registers between the two, as far as it fits; longer rows are read twice. Measured on inputs that change
+// from pass to pass: 8192 x 32000 bf16 with a tenth of the rows masked, loss and gradient 170 us (5.9 TB/s; a 2:1 stream
+// reaches 6.0), loss alone 76 to 83 (5.7 to 6.2), in two calls 241 to 248; 1023 x 50257 fp32 in two calls 117 (its rows
+// lie off 16 bytes); one row of 50257 bf16 10.4, which is a chain of loads and one CU's exponentials (two for an entry).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -33,6 +36,7 @@ struct Args {
   float slope;                // 1, or 0 where k_pairs sets it for the rows of its sequences
   double log_low, log_high;   // log of the ratio's range
   float c_hi, c_lo;           // log2(e)/T as a sum of two fp32 numbers
+  int two;                    // the second is over 2^-26 of the first
   double inv_t;
   const float* stats_in;
   const float* upstream;
@@ -45,35 +49,84 @@ struct Args {
 
 enum { kForward = 1, kBackward = 2, kStep = 3 };  // bit 0: loss, bit 1: gradient
 
-// c * d to fp32 accuracy: c in one fp32 number is off by up to 2^-25 of it with one sign for every entry,
-// which the sum's logarithm would carry into l. -inf is taken as the lowest finite number (c_lo may be
-// negative or 0, and would make a NaN of it).
+// A place on the base-2 scale that exponentials are taken from: 2^(z c - k) is 2^((z - m) c) up to a factor that is
+// the same for every z, k being m c rounded, and z c - k is one fused operation. c is one fp32 number there, which
+// takes up to 2^-26 of (m - z) c off an exponent; where it would be more (by the temperature), and where m c
+// nears fp32's end (a row of the type's lowest numbers), k is infinite and differences are formed first.
+struct From {
+  float m, k;
+};
+
+__device__ __forceinline__ From from(const Args& a, float m) {
+  const float k = m * a.c_hi;
+  return From{m, !a.two && fabsf(k) < 1e37f ? k : INFINITY};
+}
+
+// c * d to fp32 accuracy. -inf is taken as the lowest finite number (c_lo may be negative or 0, and would
+// make a NaN of it).
 __device__ __forceinline__ float mul_c(const Args& a, float d) {
   d = d < kLowest ? kLowest : d;
   return __builtin_fmaf(d, a.c_hi, d * a.c_lo);
 }
 
-// A running maximum and the sum of 2^((z - m) c). Starts at the lowest finite number, so that -inf entries add 0.
-struct MaxSum {
-  float m, s;
+template <int N>
+__device__ __forceinline__ void exponentials(const Args& a, From f, const float (&z)[N], float (&e)[N]) {
+  if (f.k < INFINITY) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = ex2(__builtin_fmaf(z[j], a.c_hi, -f.k));
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = ex2(mul_c(a, z[j] - f.m));
+  }
+}
+
+__device__ __forceinline__ float exponential(const Args& a, From f, float z) {
+  const float in[1] = {z};
+  float e[1];
+  exponentials<1>(a, f, in, e);
+  return e[0];
+}
+
+// What a sum counted from `f` is multiplied by to count from `to`.
+__device__ __forceinline__ float moved_to(const Args& a, From f, From to) {
+  return f.k < INFINITY && to.k < INFINITY ? ex2(f.k - to.k) : ex2(mul_c(a, f.m - to.m));
+}
+
+// A sum of exponentials and the place it counts from, one of the numbers seen. Starts at the lowest finite
+// number, so that -inf entries add 0.
+struct PlaceSum {
+  From f;
+  float s;
 };
 
-// Adds N values, but the one at `skip`, to a running sum.
+// Adds N values, but the one at `skip`, to a running sum. Its place moves only when the sum leaves the range (at the
+// first values, and at values 2^40 over the place): a maximum of every value would cost as much again as the
+// argument and the sum of its exponential.
 template <int N>
-__device__ __forceinline__ void add(const Args& a, MaxSum& r, float (&f)[N], uint32_t skip) {
+__device__ __forceinline__ void add(const Args& a, PlaceSum& r, float (&z)[N], uint32_t skip) {
   if (skip < N) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = skip == (uint32_t)j ? -INFINITY : f[j];
+    for (int j = 0; j < N; ++j) z[j] = skip == (uint32_t)j ? -INFINITY : z[j];
   }
-  float m = f[0];
+  float e[N], s = r.s;
+  exponentials<N>(a, r.f, z, e);
 #pragma unroll
-  for (int j = 1; j < N; ++j) m = f[j] > m ? f[j] : m;
-  if (m > r.m) {
-    r.s *= ex2(mul_c(a, r.m - m));
-    r.m = m;
+  for (int j = 0; j < N; ++j) s += e[j];
+  if (!(s < 0x1p40f)) {
+    float m = r.f.m;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = z[j] > m ? z[j] : m;
+    if (m > r.f.m) {
+      const From to = from(a, m);
+      if (r.s > 0.0f) r.s *= moved_to(a, r.f, to);
+      r.f = to;
+    }
+    s = r.s;
+    exponentials<N>(a, r.f, z, e);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s += e[j];
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) r.s += ex2(mul_c(a, f[j] - r.m));
+  r.s = s;
 }
 
 // exp(d) - 1 - d without the digits that cancel near 0
@@ -85,33 +138,81 @@ __device__ __forceinline__ float kl_term(float d) {
   return 0.5f * d * d * s;
 }
 
+// fp64 functions to about 1e-11 relative, which is what l needs: the math library's, to the last place, are
+// several times as long, and one wave of every row runs them while the row's other waves wait (8192 rows of 4096
+// fp16: loss alone 22.3 us against 23.9, in one pass with the gradient 34.2 against 37.6).
+
+// 1/x by two steps of Newton's from the approximate reciprocal
+__device__ __forceinline__ double inverse(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = fma(fma(-x, r, 1.0), r, r);
+  return fma(fma(-x, r, 1.0), r, r);
+}
+
+// 2^x for x up to 1000, by its series about the nearest whole exponent; 0 below -1100
+__device__ __forceinline__ double exp2_of(double x) {
+  x = x < -1100.0 ? -1100.0 : x;
+  const double k = rint(x), f = (x - k) * 0.69314718055994530942;
+  double p = 1.0 / 362880.0;
+  p = fma(p, f, 1.0 / 40320.0);
+  p = fma(p, f, 1.0 / 5040.0);
+  p = fma(p, f, 1.0 / 720.0);
+  p = fma(p, f, 1.0 / 120.0);
+  p = fma(p, f, 1.0 / 24.0);
+  p = fma(p, f, 1.0 / 6.0);
+  p = fma(p, f, 0.5);
+  p = fma(p, f, 1.0);
+  p = fma(p, f, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)k);
+}
+
+// log(1 + e) for e > -1/4, as k log 2 + 2 atanh(u): for e under sqrt(2) - 1 u = e/(2 + e), which keeps e's digits,
+// else u = (m - 1)/(m + 1) with 1 + e = 2^k m, m about 1. |u| is under 0.172, and the series ends at u^13/13.
+__device__ __forceinline__ double log1p_of(double e) {
+  const double v = 1.0 + e;
+  double k = 0.0, top = e, bottom = 2.0 + e;
+  if (!(e < 0.41421356)) {
+    double m = __builtin_amdgcn_frexp_mant(v);  // 1/2 to 1
+    k = (double)__builtin_amdgcn_frexp_exp(v);
+    if (m < 0.70710678) m *= 2.0, k -= 1.0;
+    top = m - 1.0;
+    bottom = m + 1.0;
+  }
+  const double u = top * inverse(bottom), q = u * u;
+  double p = 1.0 / 13.0;
+  p = fma(p, q, 1.0 / 11.0);
+  p = fma(p, q, 1.0 / 9.0);
+  p = fma(p, q, 1.0 / 7.0);
+  p = fma(p, q, 1.0 / 5.0);
+  p = fma(p, q, 1.0 / 3.0);
+  p = fma(p, q, 1.0);
+  return fma(k, 0.69314718055994530942, 2.0 * u * p);
+}
+
 // What one wave works out for a row and the others wait for.
 struct Row {
-  float top, sum;  // softmax: q_v = 2^((z_v - top) c)/sum
+  float top, sum;  // softmax: q_v = (exponential of z_v from `top`)/sum
   float slope;     // dloss/dl
   float rest;      // 1 - q of the token
 };
 
-// The row's softmax about its token from the other entries' largest m and sum s, and its loss. Run by one wave,
+// The row's softmax about its token from the other entries' sum s, counted from f, and its loss. Run by one wave,
 // every lane alike.
-__device__ __forceinline__ Row finish(const Args& a, uint64_t row, float z, float m, double s, float w, float old,
+__device__ __forceinline__ Row finish(const Args& a, uint64_t row, float z, From f, double s, float w, float old,
                                       float adv, float ref, int lane) {
   Row r;
-  double l, rest;
-  const double t = ((double)z - (double)m) * a.inv_t;
-  if (t >= 0.0) {
-    const double e = s * exp(-t);
-    l = -log1p(e);
-    rest = e / (1.0 + e);
-    r.top = z;
-    r.sum = (float)(1.0 + e);
-  } else {
-    const double total = s + exp(t);
-    l = t - log(total);
-    rest = s / total;
-    r.top = m;
-    r.sum = (float)total;
-  }
+  // k is m c rounded; the sum from m itself
+  const double off = f.k < INFINITY ? exp2_of((double)f.k - (double)f.m * (double)a.c_hi) : 1.0;
+  s *= off;
+  const double t = ((double)z - (double)f.m) * a.inv_t;
+  const bool above = t >= 0.0;  // of the others' place; below it s is at least 1 but for its rounding
+  const double near = exp2_of(-fabs(t) * 1.4426950408889634074);
+  const double e = above ? s * near : (s - 1.0) + near;
+  const double log_total = log1p_of(e);
+  double l = above ? -log_total : t - log_total;
+  double rest = (above ? e : s) * inverse(1.0 + e);
+  r.top = above ? z : f.m;
+  r.sum = above ? (float)(1.0 + e) * exponential(a, from(a, z), z) : (float)((1.0 + e) * inverse(off));
   if (z == INFINITY) l = rest = NAN, r.sum = NAN;
   if (r.sum == 0.0f) l = rest = NAN, r.sum = NAN;
   r.rest = (float)rest;
@@ -169,7 +270,7 @@ __device__ __forceinline__ void no_gradient(T* dz, uint32_t vocab, int t) {
 }
 
 // NV: 16-byte vectors of the row that a thread of the step holds in registers; 0: reads it again.
-// STREAM: the gradient goes past the caches.
+// STREAM: the logits are read and the gradient written past the caches.
 template <typename T, int MODE, int NV, int NT, bool STREAM>
 __global__ __launch_bounds__(NT) void k_token(Args a) {
   __shared__ float s_m[NT / 64];
@@ -187,7 +288,21 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
   const uint32_t body = vocab / W;     // whole vectors
   const uint32_t last = body * W + t;  // a thread's element behind them, if < vocab
 
-  // the token and the weight first, and nothing else of the row without them
+  auto load = [&](uint32_t i) -> V {
+    const V* p = reinterpret_cast<const V*>(z + (uint64_t)i * W);
+    if constexpr (STREAM && !(MODE == kStep && NV == 0)) return __builtin_nontemporal_load(p);
+    else return *p;  // (a step whose row is not held reads it again)
+  };
+  V held[NV ? NV : 1];
+  auto hold = [&]() {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i * NT + t < (int)body) held[i] = load(i * NT + t);
+  };
+  // The token and the weight first, and nothing else of the row without them; of a few rows (blocks of 1024) the row
+  // at once, as one row's latency is a chain of loads.
+  constexpr bool kEarly = NV > 0 && NT == 1024;
+  if constexpr (kEarly) hold();
   const int64_t label = in.label_bytes == 8 ? static_cast<const int64_t*>(in.label)[row]
                                             : static_cast<const int32_t*>(in.label)[row];
   const float w = (MODE & 1) && a.policy && a.p.weight ? a.p.weight[row] : 1.0f;
@@ -199,10 +314,7 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
     return;
   }
   const uint32_t y = (uint32_t)label;
-  V held[NV ? NV : 1];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (i * NT + t < (int)body) held[i] = *reinterpret_cast<const V*>(z + (uint64_t)(i * NT + t) * W);
+  if constexpr (!kEarly) hold();
 
   Row r;
   float up = a.upstream && MODE == kStep ? a.upstream[row] : 1.0f;
@@ -215,7 +327,7 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
         if (a.p.ref_logp) ref = a.p.ref_logp[row];
       }
     }
-    MaxSum rest{kLowest, 0.0f};
+    PlaceSum rest{from(a, kLowest), 0.0f};
     auto one = [&](V x, uint32_t i) {
       float f[W];
 #pragma unroll
@@ -227,32 +339,33 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
       for (int i = 0; i < NV; ++i)
         if (i * NT + t < (int)body) one(held[i], i * NT + t);
     } else {
-      uint32_t i = t;
-      for (; i + 3 * NT < body; i += 4 * NT) {
+      for (uint32_t i = t; i < body; i += 4 * NT) {
         V x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const V*>(z + (uint64_t)(i + u * NT) * W);
+        for (int u = 0; u < 4; ++u)
+          if (i + u * NT < body) x[u] = load(i + u * NT);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) one(x[u], i + u * NT);
+        for (int u = 0; u < 4; ++u)
+          if (i + u * NT < body) one(x[u], i + u * NT);
       }
-      for (; i < body; i += NT) one(*reinterpret_cast<const V*>(z + (uint64_t)i * W), i);
     }
     if (last < vocab && last != y) {
       float f[1] = {(float)z[last]};
       add<1>(a, rest, f, 1);
     }
-    const float m = wave_reduce(rest.m, kLowest, [](float p, float q) { return p > q ? p : q; });
-    const double s = wave_sum((double)(rest.s * ex2(mul_c(a, rest.m - m))));
-    if ((t & 63) == 0) s_m[wave] = m, s_s[wave] = s;
+    const From own = from(a, wave_reduce(rest.f.m, kLowest, [](float p, float q) { return p > q ? p : q; }));
+    const double s = wave_sum((double)(rest.s * moved_to(a, rest.f, own)));
+    if ((t & 63) == 0) s_m[wave] = own.m, s_s[wave] = s;
     __syncthreads();
     if (wave == 0) {
       float top = s_m[0];
 #pragma unroll
       for (int i = 1; i < NT / 64; ++i) top = s_m[i] > top ? s_m[i] : top;
+      const From all = from(a, top);
       double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < NT / 64; ++i) sum += s_s[i] * (double)ex2(mul_c(a, s_m[i] - top));
-      r = finish(a, row, zy, top, sum, w, old, adv, ref, t);
+      for (int i = 0; i < NT / 64; ++i) sum += s_s[i] * (double)moved_to(a, from(a, s_m[i]), all);
+      r = finish(a, row, zy, all, sum, w, old, adv, ref, t);
       if ((MODE & 2) && t == 0) s_row = r;
     }
     if constexpr ((MODE & 2) != 0) {
@@ -270,11 +383,16 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
 
   if constexpr ((MODE & 2) != 0) {
     const float g = a.scale * up * r.slope * (float)a.inv_t;
-    const float out = -g / r.sum, m = r.top;
+    const float out = -g / r.sum;
+    const From top = from(a, r.top);
     auto one = [&](V x, uint32_t i) {
       V v;
+      float z[W], e[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = (T)(out * ex2(mul_c(a, (float)x[j] - m)));
+      for (int j = 0; j < W; ++j) z[j] = (float)x[j];
+      exponentials<W>(a, top, z, e);
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] = (T)(out * e[j]);
       const uint32_t at = y - i * W;
       if (at < W) {
 #pragma unroll
@@ -288,17 +406,17 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
       for (int i = 0; i < NV; ++i)
         if (i * NT + t < (int)body) one(held[i], i * NT + t);
     } else {
-      uint32_t i = t;
-      for (; i + 3 * NT < body; i += 4 * NT) {
+      for (uint32_t i = t; i < body; i += 4 * NT) {
         V x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const V*>(z + (uint64_t)(i + u * NT) * W);
+        for (int u = 0; u < 4; ++u)
+          if (i + u * NT < body) x[u] = load(i + u * NT);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) one(x[u], i + u * NT);
+        for (int u = 0; u < 4; ++u)
+          if (i + u * NT < body) one(x[u], i + u * NT);
       }
-      for (; i < body; i += NT) one(*reinterpret_cast<const V*>(z + (uint64_t)i * W), i);
     }
-    if (last < vocab) dz[last] = last == y ? (T)(g * r.rest) : (T)(out * ex2(mul_c(a, (float)z[last] - m)));
+    if (last < vocab) dz[last] = last == y ? (T)(g * r.rest) : (T)(out * exponential(a, top, (float)z[last]));
   }
 }
 
@@ -306,46 +424,51 @@ __global__ __launch_bounds__(NT) void k_token(Args a) {
 
 constexpr int kPairThreads = 256;
 
-// Sums of two numbers over the block, in a fixed order, in every thread.
-__device__ __forceinline__ void block_sums(double& x, double& y, double (*lds)[2]) {
-  x = wave_sum(x), y = wave_sum(y);
-  const int wave = threadIdx.x / 64;
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) lds[wave][0] = x, lds[wave][1] = y;
-  __syncthreads();
-  x = y = 0.0;
-  for (int i = 0; i < kPairThreads / 64; ++i) x += lds[i][0], y += lds[i][1];
-}
-
 // One block per pair: the sequences' sums from the rows' l, the loss, and each row's derivative.
 __global__ __launch_bounds__(kPairThreads) void k_pairs(zero_preference p, uint64_t rows, float* stats, float* loss,
                                                         float* seq_logp) {
-  __shared__ double lds[kPairThreads / 64][2];
+  __shared__ double lds[kPairThreads / 64][4];
   const uint64_t pair = blockIdx.x;
   int64_t edge[3];
-  for (int i = 0; i < 3; ++i) {
-    const int64_t e = p.start_bytes == 8 ? static_cast<const int64_t*>(p.seq_start)[2 * pair + i]
-                                         : static_cast<const int32_t*>(p.seq_start)[2 * pair + i];
-    edge[i] = e < 0 ? 0 : e > (int64_t)rows ? (int64_t)rows : e;
-  }
-  double l[2], n[2];
-  for (int i = 0; i < 2; ++i) {
-    double sum = 0.0, count = 0.0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    edge[i] = p.start_bytes == 8 ? static_cast<const int64_t*>(p.seq_start)[2 * pair + i]
+                                 : static_cast<const int32_t*>(p.seq_start)[2 * pair + i];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) edge[i] = edge[i] < 0 ? 0 : edge[i] > (int64_t)rows ? (int64_t)rows : edge[i];
+  const float w32 = p.weight ? p.weight[pair] : 1.0f;
+  const float ref = p.ref_logp ? p.ref_logp[2 * pair] : 0.0f, ref2 = p.ref_logp ? p.ref_logp[2 * pair + 1] : 0.0f;
+  double sum[4] = {};  // each sequence's l and number of tokens
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
     for (int64_t r = edge[i] + threadIdx.x; r < edge[i + 1]; r += kPairThreads) {
       const float* o = stats + r * ZERO_TOKEN_STATS;
-      sum += (double)o[kLHigh] + (double)o[kLLow];
-      count += (double)o[kOn];
+      sum[2 * i] += (double)o[kLHigh] + (double)o[kLLow];
+      sum[2 * i + 1] += (double)o[kOn];
     }
-    block_sums(sum, count, lds);
-    n[i] = p.average && count > 0.0 ? count : 1.0;
-    l[i] = sum / n[i];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] = wave_sum(sum[k]);
+  if (threadIdx.x % 64 == 0)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) lds[threadIdx.x / 64][k] = sum[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sum[k] = 0.0;
+    for (int i = 0; i < kPairThreads / 64; ++i) sum[k] += lds[i][k];
+  }
+  double l[2], n[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    n[i] = p.average && sum[2 * i + 1] > 0.0 ? sum[2 * i + 1] : 1.0;
+    l[i] = sum[2 * i] / n[i];
   }
   double gap = l[0] - l[1];
-  if (p.ref_logp) gap -= (double)p.ref_logp[2 * pair] - (double)p.ref_logp[2 * pair + 1];
+  gap -= (double)ref - (double)ref2;
   const double x = (double)p.beta * gap - (double)p.margin, e = p.label_smoothing;
-  const double w = p.weight ? (double)p.weight[pair] : 1.0;
+  const double w = (double)w32;
   // log(1 + exp(-|x|)), and the logistic function of -|x| and |x|
-  const double far = exp(-fabs(x)), both = log1p(far);
+  const double far = exp2_of(-fabs(x) * 1.4426950408889634074), both = log1p_of(far);
   const double plus = x > 0.0 ? 0.0 : -x, minus = x > 0.0 ? x : 0.0;  // the rest of log(1 + exp(-x)), log(1 + exp(x))
   const double up = x > 0.0 ? 1.0 / (1.0 + far) : far / (1.0 + far);   // 1/(1 + exp(-x)), a NaN for one
   const double down = x > 0.0 ? far / (1.0 + far) : 1.0 / (1.0 + far);
@@ -372,13 +495,12 @@ hipError_t launch_one(const Args& a, hipStream_t s) {
   // a row a block, over two dimensions, as one holds no more than 2^32 threads
   const uint64_t wide = a.in.rows < kGridRows ? a.in.rows : kGridRows;
   const dim3 grid((unsigned)wide, (unsigned)((a.in.rows + wide - 1) / wide)), block(NT);
-  // a gradient of 128 MiB and more would push the logits out of the memory side cache; a smaller one stays for
-  // whoever reads it next
-  if constexpr ((MODE & 2) != 0) {
-    if (a.in.rows * a.in.vocab * sizeof(T) >= (128ull << 20)) {
-      k_token<T, MODE, NV, NT, true><<<grid, block, 0, s>>>(a);
-      return hipGetLastError();
-    }
+  // Logits and a gradient of 128 MiB and more go past the caches, which would hardly hold them until they are next
+  // read (8192 x 32000 bf16 loss alone 76 us, 86 through them; 1023 x 50257 fp32 36 and 38); smaller ones stay for
+  // whoever reads them next.
+  if (a.in.rows * a.in.vocab * sizeof(T) >= (128ull << 20)) {
+    k_token<T, MODE, NV, NT, true><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
   }
   k_token<T, MODE, NV, NT, false><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
@@ -388,7 +510,10 @@ template <typename T>
 hipError_t launch(const Args& a, int mode, hipStream_t s) {
   const uint64_t v = a.in.vocab / Pack<T>::n;  // vectors of a row
 #define ZERO_GO(MODE, NV, NT) return launch_one<T, MODE, NV, NT>(a, s)
-  // Few rows: 1024 threads on each, for the latency of one. Many: small blocks, several to a CU.
+  // Few rows: 1024 threads on each, for the latency of one. Many: small blocks, several to a CU, so that one's loads run
+  // under another's arithmetic and stores; but the gradient alone, which waits for nothing, in whole CUs' worth (8192 x
+  // 32000 bf16 171 us, 256 threads 193), and a row that is read twice, which so stays in the caches (2048 x 131072 bf16
+  // 230 us, 512 threads 241, held by 1024 threads 392).
   const bool wide = a.in.rows < 512;
   if (mode == kForward) {
     if (wide) ZERO_GO(kForward, 0, 1024);
@@ -396,21 +521,21 @@ hipError_t launch(const Args& a, int mode, hipStream_t s) {
     ZERO_GO(kForward, 0, 256);
   }
   if (mode == kBackward) {
-    if (wide) ZERO_GO(kBackward, 0, 1024);
-    if (v > 4096) ZERO_GO(kBackward, 0, 512);
+    if (wide || v > 2048) ZERO_GO(kBackward, 0, 1024);
     ZERO_GO(kBackward, 0, 256);
   }
   if (wide) {
     if (v <= 4 * 1024) ZERO_GO(kStep, 4, 1024);
     if (v <= 8 * 1024) ZERO_GO(kStep, 8, 1024);
+    if (v <= 16 * 1024) ZERO_GO(kStep, 16, 1024);
   } else {
-    if (v <= 4 * 256) ZERO_GO(kStep, 4, 256);
+    if (v <= 4 * 128) ZERO_GO(kStep, 4, 128);
+    if (v <= 8 * 128) ZERO_GO(kStep, 8, 128);
     if (v <= 8 * 256) ZERO_GO(kStep, 8, 256);
-    if (v <= 16 * 256) ZERO_GO(kStep, 16, 256);
-    if (v <= 28 * 256) ZERO_GO(kStep, 28, 256);
+    if (v <= 8 * 512) ZERO_GO(kStep, 8, 512);
+    if (v <= 16 * 512) ZERO_GO(kStep, 16, 512);
     if (v <= 28 * 512) ZERO_GO(kStep, 28, 512);
   }
-  if (v <= 16 * 1024) ZERO_GO(kStep, 16, 1024);
   ZERO_GO(kStep, 0, 1024);
 #undef ZERO_GO
 }
@@ -467,6 +592,7 @@ zero_status check_in(const char* fn, const zero_token_in* in, Args& a) {
   const double c = 1.4426950408889634074 / (double)in->temperature;
   a.c_hi = (float)c;
   a.c_lo = (float)(c - (double)a.c_hi);
+  a.two = fabsf(a.c_lo) > 0x1p-26f * a.c_hi;
   a.inv_t = 1.0 / (double)in->temperature;
   return ZERO_OK;
 }
