@@ -23,7 +23,9 @@ struct ForwardArgs {
 // rows without a shared gate), or one of the `chunks` parts of a segment.
 struct Plan {
   uint32_t waves;   // a row's
-  uint32_t vecs;    // groups of 8 columns that a lane holds: 1 or 2
+  uint32_t vecs;    // groups of 8 columns of a lane: 1 or 2
+  uint32_t threads; // a block's
+  bool apart;       // the sums over rows by a kernel of their own
   uint64_t segments, segs, chunks, per, chunk;  // per: rows of a segment; chunk: rows of a part
   uint64_t blocks;
 };
@@ -39,12 +41,11 @@ struct BackwardArgs {
   int32_t grad_f32, accumulate;
   float* part[kSums];  // [blocks, features] each, NULL: not wanted
   int gate_mode;       // 0: none, 1: shared by rows, 2: one a row
-  bool past_caches;
+  bool wide;           // sums without the normalised values are formed too (a layer norm, a bias's gradient)
+  float* coef;         // plan.apart: [rows, 2], what k_columns needs of each row; NULL: nothing
   Plan plan;
   hipStream_t stream;
 };
-
-constexpr int kBackThreads = 1024;
 
 template <int DT, bool S32>
 hipError_t launch_forward(const ForwardArgs& a);

@@ -61,15 +61,20 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
   }
 }
 
-// A row's waves hold 8 columns a lane, and twice that above 8192 columns. A block of 16 waves takes 16/waves
-// rows at a time; about one block for each compute unit.
-Plan plan_of(uint64_t rows, uint64_t features, uint64_t segment) {
+// A row's waves hold 8 columns a lane, or 16. About one block for each compute unit, each for as many rows at a time
+// as it has waves for. Blocks of 16 waves hide more of the loads' latency, those of 8 leave each lane 256 registers
+// in place of 128, which the variants with more sums over rows need (8192 x 4096 bf16 without biases 92 us, 99 in blocks
+// of 8 waves; with two layer norms, their biases and a gate 113, 147 in blocks of 16). Above 8192 columns the sums are
+// formed apart.
+Plan plan_of(uint64_t rows, uint64_t features, uint64_t segment, bool many) {
   Plan p{};
   const uint64_t vecs = (features + 7) / 8;
-  p.vecs = vecs <= 1024 ? 1 : 2;
+  p.apart = vecs > 1024;
+  p.threads = p.apart || !many ? 1024 : 512;
+  p.vecs = vecs <= p.threads ? 1 : 2;
   p.waves = 1;
   while ((uint64_t)p.waves * 64 * p.vecs < vecs) p.waves *= 2;
-  const uint64_t groups = kBackThreads / 64 / p.waves;
+  const uint64_t groups = p.threads / 64 / p.waves;
   const uint64_t want = std::max((rows + 255) / 256, groups);  // rows of a block
   p.per = std::min(segment, rows);
   p.segments = (rows + p.per - 1) / p.per;
@@ -89,6 +94,9 @@ Plan plan_of(uint64_t rows, uint64_t features, uint64_t segment) {
 }
 
 uint64_t part_bytes(const Plan& p, uint64_t features) { return (p.blocks * features * 4 + 15) & ~15ull; }
+
+// What k_columns needs of each row, behind the parts.
+uint64_t coef_bytes(uint64_t rows, uint64_t features) { return features > 8192 ? (rows * 8 + 15) & ~15ull : 0; }
 
 struct Arr {
   const char* name;
@@ -216,9 +224,11 @@ zero_status zero_norm_forward(const zero_norm_block* b, const void* x, uint64_t 
 
 uint64_t zero_norm_workspace_bytes(uint64_t rows, uint64_t features, uint64_t gate_rows) {
   if (rows == 0 || features == 0 || rows > kMaxRows || features > ZERO_NORM_MAX_FEATURES) return 0;
-  // the larger of what a gate shared by gate_rows rows and no shared gate need
-  const uint64_t shared = part_bytes(plan_of(rows, features, gate_rows ? gate_rows : rows), features);
-  return kSums * std::max(shared, part_bytes(plan_of(rows, features, rows), features));
+  // the largest of what a gate shared by gate_rows rows and no shared gate need, with few sums and with many
+  uint64_t most = 0;
+  for (const uint64_t segment : {gate_rows ? gate_rows : rows, rows})
+    for (const bool many : {false, true}) most = std::max(most, part_bytes(plan_of(rows, features, segment, many), features));
+  return kSums * most + coef_bytes(rows, features);
 }
 
 zero_status zero_norm_backward(const zero_norm_block* b, const float* stats, const void* y, uint64_t ldy, const void* dy,
@@ -268,9 +278,11 @@ zero_status zero_norm_backward(const zero_norm_block* b, const float* stats, con
   arr[n++] = Arr{"dpre_weight", dpre_weight, 1, d, d, gb, true};
   arr[n++] = Arr{"dpre_bias", dpre_bias, 1, d, d, gb, true};
   const bool shared = b->gate && gates < R;
-  const Plan p = R ? plan_of(R, d, shared ? b->gate_rows : R) : Plan{};
+  a.wide = b->post == ZERO_NORM_LAYER || b->pre == ZERO_NORM_LAYER || dpost_bias || dpre_bias || (shared && b->post_bias);
+  const Plan p = R ? plan_of(R, d, shared ? b->gate_rows : R, a.wide || (b->gate && !shared)) : Plan{};
   a.gate_mode = !b->gate ? 0 : shared ? 1 : 2;
-  const bool any_sum = dpost_weight || dpost_bias || dpre_weight || dpre_bias || (dgate && shared && p.chunks > 1);
+  const bool any_sum =
+      dpost_weight || dpost_bias || dpre_weight || dpre_bias || (dgate && shared && (p.chunks > 1 || p.apart));
   const uint64_t need = R && any_sum ? zero_norm_workspace_bytes(R, d, b->gate ? b->gate_rows : R) : 0;
   if (need) {
     if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)
@@ -300,11 +312,11 @@ zero_status zero_norm_backward(const zero_norm_block* b, const float* stats, con
                    R == 0 ? 0u : (uint32_t)(k == kGate ? p.chunks : p.blocks)};
     outs += rows_out;
   }
+  if (need && p.apart) a.coef = reinterpret_cast<float*>(static_cast<char*>(workspace) + kSums * each);
   (void)hipGetLastError();
   hipError_t e = hipSuccess;
   if (R) {
     const bool s32 = b->stream_dtype == ZERO_F32;
-    a.past_caches = R * d * (sb + 2) >= (128ull << 20);
     if (b->dtype == ZERO_BF16) e = s32 ? launch_backward<ZERO_BF16, true>(a) : launch_backward<ZERO_BF16, false>(a);
     else e = s32 ? launch_backward<ZERO_F16, true>(a) : launch_backward<ZERO_F16, false>(a);
   }

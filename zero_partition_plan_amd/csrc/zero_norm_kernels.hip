@@ -54,23 +54,35 @@ struct Eight<float> {
 // Columns that exist behind column c of d: 8 but at a row's end.
 __device__ __forceinline__ int have_of(uint32_t d, uint32_t c) { return c + 8 <= d ? 8 : c < d ? (int)(d - c) : 0; }
 
-template <typename T>
-__device__ __forceinline__ Eight<T> load8(const T* p, int have, float fill = 0.0f) {
+template <typename T, bool PAST = false>
+__device__ __forceinline__ Eight<T> load_all(const T* p) {
+  typedef typename Eight<T>::vec V;
   Eight<T> r;
-  if (have == 8) {
-    if constexpr (sizeof(T) == 4) {
-      r.v[0] = *reinterpret_cast<const typename Eight<T>::vec*>(p);
-      r.v[1] = *reinterpret_cast<const typename Eight<T>::vec*>(p + 4);
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (PAST) {
+      r.v[0] = __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+      r.v[1] = __builtin_nontemporal_load(reinterpret_cast<const V*>(p + 4));
     } else {
-      r.v = *reinterpret_cast<const typename Eight<T>::vec*>(p);
+      r.v[0] = *reinterpret_cast<const V*>(p);
+      r.v[1] = *reinterpret_cast<const V*>(p + 4);
     }
   } else {
+    if constexpr (PAST) r.v = __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+    else r.v = *reinterpret_cast<const V*>(p);
+  }
+  return r;
+}
+
+// 8 columns of which `have` exist; the others 0.
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T* p, int have) {
+  if (have == 8) return load_all<T>(p);
+  Eight<T> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const T x = j < have ? p[j] : (T)fill;
-      if constexpr (sizeof(T) == 4) r.v[j / 4][j % 4] = x;
-      else r.v[j] = x;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const T x = j < have ? p[j] : (T)0.0f;
+    if constexpr (sizeof(T) == 4) r.v[j / 4][j % 4] = x;
+    else r.v[j] = x;
   }
   return r;
 }
@@ -221,66 +233,93 @@ __global__ __launch_bounds__(1024) void k_forward(ForwardArgs a, uint32_t gate_s
     *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(post_mean, post_rstd, mean, rstd);
 }
 
+// Keeps what is computed from x from being formed earlier and held in registers.
+template <typename T>
+__device__ __forceinline__ void again(Eight<T>& x) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  u4 v[sizeof(Eight<T>) / 16];
+  __builtin_memcpy(v, &x, sizeof(x));
+#pragma unroll
+  for (auto& q : v) asm volatile("" : "+v"(q));
+  __builtin_memcpy(&x, v, sizeof(x));
+}
+
 // What of a row's arrays a lane holds.
-template <typename T, typename S, int NV, int GATE>
+template <typename T, typename S, int GATE>
 struct Held {
-  Eight<S> y[NV], dy[NV];
-  Eight<T> dh[NV], o[NV], g[GATE == 2 ? NV : 1];
-  float4 st;
+  Eight<S> y, dy;
+  Eight<T> dh, o, g;
 };
 
-// LN: a mean is taken off in one of the norms. GATE: as gate_mode.
-template <typename T, typename S, int NV, bool LN, int GATE>
-__global__ __launch_bounds__(kBackThreads) void k_backward(BackwardArgs a) {
-  constexpr int kWaves = kBackThreads / 64;
+// LN: a mean is taken off in one of the norms, or a bias has a gradient. GATE: as gate_mode. WHOLE: the columns are
+// a multiple of 8, so every lane's are all there or none are.
+//
+// The sums over rows are four at most: of dh*xh and dh, and of E*oh and E with E = D, times the row's gate where
+// every row has its own. Where rows share a gate, the gradients of that gate and of the post norm's parameters
+// are E*oh's and E's sums times the one or the others.
+// NT threads a block. SUMS: forms the sums over rows; else it leaves each row's m1 and c1 for k_columns.
+template <typename T, typename S, int NV, bool LN, int GATE, bool WHOLE, int NT, bool SUMS>
+__global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
+  constexpr int kWaves = NT / 64;
   constexpr int kOut = LN ? 8 : 4;  // sums of a row
   __shared__ __attribute__((aligned(16))) float lds[2][kWaves][kOut];
-  __shared__ __attribute__((aligned(16))) float cols[kBackThreads * 8];
+  __shared__ __attribute__((aligned(16))) float cols[LN ? 2 : 1][SUMS ? NT * 8 : 4];
   const zero_norm_block& b = a.b;
   const uint32_t d = (uint32_t)b.features, W = a.plan.waves, groups = kWaves / W;
-  const uint32_t lanes = W * 64, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int wave = threadIdx.x / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // the same in its lanes: a row's addresses are scalars
+  const uint32_t lanes = W * 64, group = wave / W, lane = threadIdx.x % lanes;
   const float inv_n = 1.0f / (float)d;
   const bool pre = b.pre != ZERO_NORM_NONE, post = b.post != ZERO_NORM_NONE, has_o = b.branch != nullptr;
   const float scale = has_o ? b.residual_scale : 1.0f;
   uint32_t col[NV];
   int have[NV];
-  Eight<T> wpre[NV], wpost[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     col[i] = (i * lanes + lane) * 8;
     have[i] = have_of(d, col[i]);
-    // 1 without a weight; 0 behind the row's end, so that nothing there counts
-    const T* w = static_cast<const T*>(b.pre_weight);
-    wpre[i] = load8<T>(w ? w + col[i] : nullptr, w ? have[i] : 0, 0.0f);
-    const T* u = static_cast<const T*>(b.post_weight);
-    wpost[i] = load8<T>(u ? u + col[i] : nullptr, u ? have[i] : 0, 0.0f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!w && j < have[i]) wpre[i].v[j] = (T)1.0f;
-      if (!u && j < have[i]) wpost[i].v[j] = (T)1.0f;
-    }
   }
-  float s_post_w[NV][8] = {}, s_pre_w[NV][8] = {}, s_gate[NV][8] = {};
-  float s_post_b[LN ? NV : 1][8] = {}, s_pre_b[LN ? NV : 1][8] = {};
+  // a parameter's columns: 1 without it, and 0 behind the row's end, so that nothing there counts
+  auto weight = [&](const void* p, int i) {
+    const T* w = static_cast<const T*>(p);
+    Eight<T> r = load8<T>(w ? w + (have[i] ? col[i] : 0u) : nullptr, w ? have[i] : 0);
+    if (!w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r.v[j] = j < have[i] ? (T)1.0f : (T)0.0f;
+    }
+    return r;
+  };
+  Eight<T> wpre[NV], wpost[NV], gate[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) wpre[i] = weight(b.pre_weight, i), wpost[i] = weight(b.post_weight, i);
+  float s_xh[NV][8] = {}, s_oh[NV][8] = {};
+  float s_dh[LN ? NV : 1][8] = {}, s_e[LN ? NV : 1][8] = {};
 
-  // The block's sums of one array, group by group, in column order; `to` takes column c's sum.
-  auto joined = [&](float (&s)[NV][8], auto to) {
+  // The block's sums of one or two arrays, group by group, in column order; `to` takes column c's.
+  auto joined = [&](float (&s)[NV][8], float (*s2)[8], auto to) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; j += 4)
-        *reinterpret_cast<float4*>(cols + (group * lanes + lane) * 8 + j) = make_float4(s[i][j], s[i][j + 1], s[i][j + 2], s[i][j + 3]);
+      for (int j = 0; j < 8; j += 4) {
+        const uint32_t at = (group * lanes + lane) * 8 + j;
+        *reinterpret_cast<float4*>(cols[0] + at) = make_float4(s[i][j], s[i][j + 1], s[i][j + 2], s[i][j + 3]);
+        if (s2) *reinterpret_cast<float4*>(cols[LN ? 1 : 0] + at) = make_float4(s2[i][j], s2[i][j + 1], s2[i][j + 2], s2[i][j + 3]);
+      }
       __syncthreads();
-      for (uint32_t c = threadIdx.x; c < lanes * 8; c += kBackThreads) {
-        float t = 0.0f;
-        for (uint32_t g = 0; g < groups; ++g) t += cols[g * lanes * 8 + c];
+      for (uint32_t c = threadIdx.x; c < lanes * 8; c += NT) {
+        float t = 0.0f, t2 = 0.0f;
+        for (uint32_t g = 0; g < groups; ++g) {
+          t += cols[0][g * lanes * 8 + c];
+          if (s2) t2 += cols[LN ? 1 : 0][g * lanes * 8 + c];
+        }
         const uint32_t at = i * lanes * 8 + c;
-        if (at < d) to(at, t);
+        if (at < d) to(at, t, t2);
       }
     }
   };
+  float* const part_pw = a.part[kPostW] ? a.part[kPostW] + (uint64_t)blockIdx.x * d : nullptr;
+  float* const part_pb = a.part[kPostB] ? a.part[kPostB] + (uint64_t)blockIdx.x * d : nullptr;
+  float* const part_g = a.part[kGate] ? a.part[kGate] + (uint64_t)blockIdx.x * d : nullptr;
 
   const uint64_t part = a.plan.chunks > 1 ? blockIdx.x % a.plan.chunks : 0;
   const uint64_t seg0 = a.plan.chunks > 1 ? blockIdx.x / a.plan.chunks : (uint64_t)blockIdx.x * a.plan.segs;
@@ -291,44 +330,67 @@ __global__ __launch_bounds__(kBackThreads) void k_backward(BackwardArgs a) {
     uint64_t end = part + 1 == a.plan.chunks ? (seg + 1) * a.plan.per : first + a.plan.chunk;
     if (end > (seg + 1) * a.plan.per) end = (seg + 1) * a.plan.per;
     if (end > b.rows) end = b.rows;
-    Eight<T> gate[GATE == 1 ? NV : 1];
+    const T* seg_gate = GATE == 1 ? static_cast<const T*>(b.gate) + seg * b.ld_gate : nullptr;
     if constexpr (GATE == 1) {
-      const T* g = static_cast<const T*>(b.gate) + seg * b.ld_gate;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) gate[i] = load8<T>(g + col[i], have[i]);
+      for (int i = 0; i < NV; ++i) gate[i] = weight(seg_gate, i);
     }
-    auto load = [&](uint64_t row) {
-      Held<T, S, NV, GATE> r;
-      const bool on = row < end;
-      if (on) r.st = *reinterpret_cast<const float4*>(a.stats + 4 * row);
-      else r.st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int n = on ? have[i] : 0;
-        r.dy[i] = load8<S>(static_cast<const S*>(a.dy) + (a.dy ? row * a.lddy + col[i] : 0), a.dy ? n : 0);
-        r.dh[i] = load8<T>(static_cast<const T*>(a.dh) + (pre ? row * a.lddh + col[i] : 0), pre ? n : 0);
-        r.y[i] = load8<S>(static_cast<const S*>(a.y) + (pre ? row * a.ldy + col[i] : 0), pre ? n : 0);
-        r.o[i] = load8<T>(static_cast<const T*>(b.branch) + (has_o ? row * b.ld_branch + col[i] : 0), has_o ? n : 0);
-        if constexpr (GATE == 2) r.g[i] = load8<T>(static_cast<const T*>(b.gate) + row * b.ld_gate + col[i], n);
-      }
+    // The parameters' columns of vector i: held, but what is formed of them is formed anew in each pass.
+    auto parameters = [&](int i) {
+      again(wpre[i]), again(wpost[i]);
+      if constexpr (GATE == 1) again(gate[i]);
+    };
+    // A vector of a row's arrays. Rows behind the end, and lanes behind the row's, read what is there: nothing of it
+    // counts (their weights are 0), and loads without conditions go out together, a row ahead of their use.
+    auto load = [&](uint64_t row, int i) {
+      Held<T, S, GATE> r{};
+      row = row < end ? row : end - 1;
+      const uint32_t c = have[i] ? col[i] : 0u;
+      auto eight = [&](auto* p) {
+        typedef typename std::remove_const<typename std::remove_pointer<decltype(p)>::type>::type E;
+        // past the caches what is not read again
+        if constexpr (WHOLE) return load_all<E, SUMS>(p);
+        else return load8<E>(p, have[i]);
+      };
+      if (a.dy) r.dy = eight(static_cast<const S*>(a.dy) + row * a.lddy + c);
+      if (pre) r.dh = eight(static_cast<const T*>(a.dh) + row * a.lddh + c);
+      if (pre) r.y = eight(static_cast<const S*>(a.y) + row * a.ldy + c);
+      if (has_o) r.o = eight(static_cast<const T*>(b.branch) + row * b.ld_branch + c);
+      if constexpr (GATE == 2) r.g = eight(static_cast<const T*>(b.gate) + row * b.ld_gate + c);
       return r;
     };
+    // the next row's arrays are asked for before this one's are used, where the registers hold both
+    Held<T, S, GATE> ahead[NV];
+    float4 st_ahead;
+    auto look = [&](uint64_t row) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ahead[i] = load(row, i);
+      st_ahead = *reinterpret_cast<const float4*>(a.stats + 4 * (row < end ? row : end - 1));
+    };
+    if (SUMS && first < end) look(first + group);
     for (uint64_t base_row = first; base_row < end; base_row += groups) {
       const uint64_t row = base_row + group;
       const bool on = row < end;
-      const Held<T, S, NV, GATE> r = load(row);
-      const float mo = post ? r.st.x : 0.0f, ro = post ? r.st.y : 1.0f;
-      const float mp = pre ? r.st.z : 0.0f, rp = pre ? r.st.w : 0.0f;
+      if (!SUMS) look(row);
+      Held<T, S, GATE> held[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) held[i] = ahead[i];
+      const float4 st = st_ahead;
+      if (SUMS && base_row + groups < end) look(row + groups);
+      const float mo = post ? st.x : 0.0f, ro = post ? st.y : 1.0f;
+      const float mp = pre ? st.z : 0.0f, rp = pre ? st.w : 0.0f;
       float sum[kOut] = {};
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        parameters(i);
+        const Held<T, S, GATE>& r = held[i];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float xh = (r.y[i][j] - mp) * rp, gh = r.dh[i][j] * wpre[i][j];
-          const float base = r.dy[i][j] + rp * gh, oh = (r.o[i][j] - mo) * ro;
+          const float xh = (r.y[j] - mp) * rp, gh = r.dh[j] * wpre[i][j];
+          const float base = r.dy[j] + rp * gh, oh = (r.o[j] - mo) * ro;
           float q = b.branch_scale * wpost[i][j];
           if constexpr (GATE == 1) q *= gate[i][j];
-          if constexpr (GATE == 2) q *= r.g[i][j];
+          if constexpr (GATE == 2) q *= r.g[j];
           const float p = q * oh;
           sum[0] += gh * xh;
           sum[1] += p * base;
@@ -341,6 +403,7 @@ __global__ __launch_bounds__(kBackThreads) void k_backward(BackwardArgs a) {
             sum[7] += p;
           }
         }
+      }
 #pragma unroll
       for (int k = 0; k < (LN ? 8 : 3); ++k) sum[k] = wave_sum(sum[k]);
       if (W > 1) {
@@ -364,109 +427,231 @@ __global__ __launch_bounds__(kBackThreads) void k_backward(BackwardArgs a) {
       float c2 = 0.0f, m2 = 0.0f;
       if (post) c2 = (sum[1] - rp * ((LN ? m1 * sum[LN ? 7 : 0] : 0.0f) + c1 * sum[2])) * inv_n;
       if (LN && b.post == ZERO_NORM_LAYER) m2 = (sum[LN ? 4 : 0] - rp * (m1 * sum[LN ? 6 : 0] + c1 * sum[LN ? 5 : 0])) * inv_n;
+      if (!on) continue;
+      if (!SUMS && a.coef && lane == 0) *reinterpret_cast<float2*>(a.coef + 2 * row) = make_float2(m1, c1);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        parameters(i);
+        Held<T, S, GATE>& r = held[i];
+        again(r.y), again(r.dy), again(r.dh), again(r.o);
+        if constexpr (GATE == 2) again(r.g);
         float dx[8], db[8], dg[8];
         Eight<T> bias{};
-        if (GATE != 0 && b.post_bias) bias = load8<T>(static_cast<const T*>(b.post_bias) + col[i], have[i]);
+        if (GATE == 2 && a.dgate && b.post_bias) bias = load8<T>(static_cast<const T*>(b.post_bias) + (have[i] ? col[i] : 0u), have[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float dh = r.dh[i][j];
-          const float xh = (r.y[i][j] - mp) * rp;
-          const float D = r.dy[i][j] + rp * (dh * wpre[i][j]) - rp * (m1 + xh * c1);
-          const float oh = (r.o[i][j] - mo) * ro;
-          float u = b.branch_scale * D;
-          if (GATE != 0) dg[j] = u * (oh * wpost[i][j] + (b.post_bias ? bias[j] : 0.0f));
+          const float dh = r.dh[j];
+          const float xh = (r.y[j] - mp) * rp;
+          const float D = r.dy[j] + rp * (dh * wpre[i][j]) - rp * (m1 + xh * c1);
+          const float oh = (r.o[j] - mo) * ro;
+          float e = D;
+          if constexpr (GATE == 2) {
+            dg[j] = b.branch_scale * D * (oh * wpost[i][j] + bias[j]);
+            e *= r.g[j];
+          }
+          float u = b.branch_scale * e * wpost[i][j];
           if constexpr (GATE == 1) u *= gate[i][j];
-          if constexpr (GATE == 2) u *= r.g[i][j];
           dx[j] = scale * D;
-          db[j] = ro * (u * wpost[i][j] - m2 - oh * c2);
-          if (on) {
-            s_pre_w[i][j] += dh * xh;
-            s_post_w[i][j] += u * oh;
-            if constexpr (LN) {
-              s_pre_b[i][j] += dh;
-              s_post_b[i][j] += u;
-            }
-            if constexpr (GATE == 1) s_gate[i][j] += dg[j];
+          db[j] = ro * (u - m2 - oh * c2);
+          if constexpr (SUMS) {
+            s_xh[i][j] += dh * xh;
+            s_oh[i][j] += e * oh;
+          }
+          if constexpr (SUMS && LN) {
+            s_dh[i][j] += dh;
+            s_e[i][j] += e;
           }
         }
-        if (on) {
-          if (a.dx) store8<S>(static_cast<S*>(a.dx) + row * a.lddx + col[i], have[i], dx, a.past_caches);
-          if (a.dbranch) store8<T>(static_cast<T*>(a.dbranch) + row * a.lddbranch + col[i], have[i], db, a.past_caches);
-          if (GATE == 2 && a.dgate) {
-            const uint64_t at = row * a.lddgate + col[i];
-            if (a.grad_f32) {
-              float* o = static_cast<float*>(a.dgate) + at;
-              if (a.accumulate) {
-                const Eight<float> was = load8<float>(o, have[i]);
+        if (a.dx) store8<S>(static_cast<S*>(a.dx) + row * a.lddx + col[i], have[i], dx, false);
+        if (a.dbranch) store8<T>(static_cast<T*>(a.dbranch) + row * a.lddbranch + col[i], have[i], db, false);
+        if (GATE == 2 && a.dgate) {
+          const uint64_t at = row * a.lddgate + col[i];
+          if (a.grad_f32) {
+            float* o = static_cast<float*>(a.dgate) + at;
+            if (a.accumulate) {
+              const Eight<float> was = load8<float>(o, have[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dg[j] += was[j];
-              }
-              store8<float>(o, have[i], dg, false);
-            } else {
-              T* o = static_cast<T*>(a.dgate) + at;
-              if (a.accumulate) {
-                const Eight<T> was = load8<T>(o, have[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dg[j] += was[j];
-              }
-              store8<T>(o, have[i], dg, false);
+              for (int j = 0; j < 8; ++j) dg[j] += was[j];
             }
+            store8<float>(o, have[i], dg, false);
+          } else {
+            T* o = static_cast<T*>(a.dgate) + at;
+            if (a.accumulate) {
+              const Eight<T> was = load8<T>(o, have[i]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) dg[j] += was[j];
+            }
+            store8<T>(o, have[i], dg, false);
           }
         }
       }
     }
-    if constexpr (GATE == 1) {
-      if (a.plan.chunks > 1 || a.part[kGate]) {
-        if (a.part[kGate])
-          joined(s_gate, [&](uint32_t c, float t) { a.part[kGate][(uint64_t)blockIdx.x * d + c] = t; });
-      } else if (a.dgate) {
-        joined(s_gate, [&](uint32_t c, float t) {
+    if constexpr (SUMS && GATE == 1) {
+      // the segment's: its gate's gradient or part of it, and its share of the post norm's
+      const bool more = seg > seg0;
+      joined(s_oh, LN ? s_e : nullptr, [&](uint32_t c, float t, float t2) {
+        const float w = b.post_weight ? (float)static_cast<const T*>(b.post_weight)[c] : 1.0f;
+        const float bias = b.post_bias ? (float)static_cast<const T*>(b.post_bias)[c] : 0.0f;
+        const float g = b.branch_scale * (float)static_cast<const T*>(b.gate)[seg * b.ld_gate + c];
+        const float dg = b.branch_scale * (w * t + bias * t2);
+        if (part_pw) part_pw[c] = (more ? part_pw[c] : 0.0f) + g * t;
+        if (part_pb) part_pb[c] = (more ? part_pb[c] : 0.0f) + g * t2;
+        if (part_g) {
+          part_g[c] = dg;
+        } else if (a.dgate) {
           const uint64_t at = seg * a.lddgate + c;
           if (a.grad_f32) {
             float* o = static_cast<float*>(a.dgate) + at;
-            *o = a.accumulate ? *o + t : t;
+            *o = a.accumulate ? *o + dg : dg;
           } else {
             T* o = static_cast<T*>(a.dgate) + at;
-            *o = (T)(a.accumulate ? (float)*o + t : t);
+            *o = (T)(a.accumulate ? (float)*o + dg : dg);
           }
-        });
+        }
+      });
+      if (seg + 1 < seg1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s_gate[i][j] = 0.0f;
+          for (int j = 0; j < 8; ++j) {
+            s_oh[i][j] = 0.0f;
+            if constexpr (LN) s_e[i][j] = 0.0f;
+          }
       }
     }
   }
-  auto leave = [&](int k, float (&s)[NV][8]) {
-    if (a.part[k]) joined(s, [&](uint32_t c, float t) { a.part[k][(uint64_t)blockIdx.x * d + c] = t; });
-  };
-  leave(kPostW, s_post_w);
-  leave(kPreW, s_pre_w);
-  if constexpr (LN) {
-    leave(kPostB, s_post_b);
-    leave(kPreB, s_pre_b);
-  }
+  if constexpr (!SUMS) return;
+  if (GATE != 1 && (part_pw || part_pb))
+    joined(s_oh, LN ? s_e : nullptr, [&](uint32_t c, float t, float t2) {
+      if (part_pw) part_pw[c] = b.branch_scale * t;
+      if (part_pb) part_pb[c] = b.branch_scale * t2;
+    });
+  if (a.part[kPreW] || a.part[kPreB])
+    joined(s_xh, LN ? s_dh : nullptr, [&](uint32_t c, float t, float t2) {
+      const uint64_t at = (uint64_t)blockIdx.x * d + c;
+      if (a.part[kPreW]) a.part[kPreW][at] = t;
+      if (a.part[kPreB]) a.part[kPreB][at] = t2;
+    });
 }
 
-template <typename T, typename S, int NV>
-hipError_t backward_of(const BackwardArgs& a) {
-  // biases are summed by the general variant only
-  const bool ln = a.b.post == ZERO_NORM_LAYER || a.b.pre == ZERO_NORM_LAYER || a.part[kPostB] || a.part[kPreB];
-  const dim3 grid((unsigned)a.plan.blocks), block(kBackThreads);
-#define ZERO_GO(LN, GATE) k_backward<T, S, NV, LN, GATE><<<grid, block, 0, a.stream>>>(a)
-  if (ln) {
-    if (a.gate_mode == 0) ZERO_GO(true, 0);
-    else if (a.gate_mode == 1) ZERO_GO(true, 1);
-    else ZERO_GO(true, 2);
-  } else {
-    if (a.gate_mode == 0) ZERO_GO(false, 0);
-    else if (a.gate_mode == 1) ZERO_GO(false, 1);
-    else ZERO_GO(false, 2);
+// The sums over rows where a row takes so many registers that k_backward cannot hold them beside it: each thread
+// walks its 8 columns down the block's rows, with each row's m1 and c1 from k_backward, and reads the arrays
+// again (4096 x 12288 with an fp32 stream and a layer norm ZERO_MEASURED us; held in one kernel, and so partly in
+// memory, 735).
+constexpr int kColumnThreads = 256;
+
+template <typename T, typename S, int GATE>
+__global__ __launch_bounds__(kColumnThreads) void k_columns(BackwardArgs a) {
+  const zero_norm_block& b = a.b;
+  const uint32_t d = (uint32_t)b.features, c = (blockIdx.y * kColumnThreads + threadIdx.x) * 8;
+  const int have = have_of(d, c);
+  if (!have) return;
+  const bool pre = b.pre != ZERO_NORM_NONE, post = b.post != ZERO_NORM_NONE;
+  const bool sum_pre = a.part[kPreW] || a.part[kPreB];
+  const bool sum_post = a.part[kPostW] || a.part[kPostB] || (GATE == 1 && a.dgate);
+  const Eight<T> wpre = load8<T>(static_cast<const T*>(b.pre_weight) + (b.pre_weight ? c : 0u), b.pre_weight ? have : 0);
+  float s_xh[8] = {}, s_dh[8] = {}, p_w[8] = {}, p_b[8] = {};
+  const uint64_t part = a.plan.chunks > 1 ? blockIdx.x % a.plan.chunks : 0;
+  const uint64_t seg0 = a.plan.chunks > 1 ? blockIdx.x / a.plan.chunks : (uint64_t)blockIdx.x * a.plan.segs;
+  const uint64_t seg1 = a.plan.chunks > 1 ? seg0 + 1 : seg0 + a.plan.segs < a.plan.segments ? seg0 + a.plan.segs : a.plan.segments;
+  for (uint64_t seg = seg0; seg < seg1; ++seg) {
+    const uint64_t first = seg * a.plan.per + part * a.plan.chunk;
+    uint64_t end = part + 1 == a.plan.chunks ? (seg + 1) * a.plan.per : first + a.plan.chunk;
+    if (end > (seg + 1) * a.plan.per) end = (seg + 1) * a.plan.per;
+    if (end > b.rows) end = b.rows;
+    float s_oh[8] = {}, s_e[8] = {};
+#pragma unroll 2
+    for (uint64_t row = first; row < end; ++row) {
+      const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * row);
+      const float mo = post ? st.x : 0.0f, ro = post ? st.y : 1.0f;
+      const float mp = pre ? st.z : 0.0f, rp = pre ? st.w : 0.0f;
+      Eight<S> y{}, dy{};
+      Eight<T> dh{}, o{}, g{};
+      if (pre) dh = load8<T>(static_cast<const T*>(a.dh) + row * a.lddh + c, have);
+      if (pre) y = load8<S>(static_cast<const S*>(a.y) + row * a.ldy + c, have);
+      float2 k = make_float2(0.0f, 0.0f);
+      if (sum_post) {
+        k = *reinterpret_cast<const float2*>(a.coef + 2 * row);
+        if (a.dy) dy = load8<S>(static_cast<const S*>(a.dy) + row * a.lddy + c, have);
+        o = load8<T>(static_cast<const T*>(b.branch) + row * b.ld_branch + c, have);
+        if constexpr (GATE == 2) g = load8<T>(static_cast<const T*>(b.gate) + row * b.ld_gate + c, have);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (y[j] - mp) * rp;
+        s_xh[j] += dh[j] * xh;
+        s_dh[j] += dh[j];
+        if (sum_post) {
+          const float w = b.pre_weight ? wpre[j] : 1.0f;
+          float e = dy[j] + rp * (dh[j] * w) - rp * (k.x + xh * k.y);
+          if constexpr (GATE == 2) e *= g[j];
+          s_oh[j] += e * ((o[j] - mo) * ro);
+          s_e[j] += e;
+        }
+      }
+    }
+    if (!sum_post) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= have) continue;
+      float g = b.branch_scale;
+      if constexpr (GATE == 1) {
+        const float w = b.post_weight ? (float)static_cast<const T*>(b.post_weight)[c + j] : 1.0f;
+        const float bias = b.post_bias ? (float)static_cast<const T*>(b.post_bias)[c + j] : 0.0f;
+        const float dg = b.branch_scale * (w * s_oh[j] + bias * s_e[j]);
+        g *= (float)static_cast<const T*>(b.gate)[seg * b.ld_gate + c + j];
+        const uint64_t at = seg * a.lddgate + c + j;
+        if (a.part[kGate]) {
+          a.part[kGate][(uint64_t)blockIdx.x * d + c + j] = dg;
+        } else if (a.dgate && a.grad_f32) {
+          float* out = static_cast<float*>(a.dgate) + at;
+          *out = a.accumulate ? *out + dg : dg;
+        } else if (a.dgate) {
+          T* out = static_cast<T*>(a.dgate) + at;
+          *out = (T)(a.accumulate ? (float)*out + dg : dg);
+        }
+      }
+      p_w[j] += g * s_oh[j];
+      p_b[j] += g * s_e[j];
+    }
   }
-#undef ZERO_GO
+  auto leave = [&](int k, const float (&s)[8]) {
+    if (!a.part[k]) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < have) a.part[k][(uint64_t)blockIdx.x * d + c + j] = s[j];
+  };
+  leave(kPostW, p_w), leave(kPostB, p_b), leave(kPreW, s_xh), leave(kPreB, s_dh);
+}
+
+template <typename T, typename S, int NV, bool LN, int GATE, int NT, bool SUMS>
+hipError_t rows_of(const BackwardArgs& a) {
+  const dim3 grid((unsigned)a.plan.blocks), block(NT);
+  if (a.b.features % 8 == 0) k_backward<T, S, NV, LN, GATE, true, NT, SUMS><<<grid, block, 0, a.stream>>>(a);
+  else k_backward<T, S, NV, LN, GATE, false, NT, SUMS><<<grid, block, 0, a.stream>>>(a);
   return hipGetLastError();
+}
+
+template <typename T, typename S, bool LN, int GATE>
+hipError_t backward_of(const BackwardArgs& a) {
+  // as plan_of chose the threads and the vectors
+  if (a.plan.apart) {
+    const bool post = a.part[kPostW] || a.part[kPostB] || (GATE == 1 && a.dgate);
+    const bool sums = post || a.part[kPreW] || a.part[kPreB];
+    // dx over dy: the sums read dy first, after a pass that leaves the rows' m1 and c1 alone
+    const bool over = post && a.dx && a.dx == a.dy;
+    BackwardArgs first = a, last = a;
+    if (over) first.dx = first.dbranch = nullptr, first.dgate = GATE == 1 ? first.dgate : nullptr;
+    hipError_t e = rows_of<T, S, 2, LN, GATE, 1024, false>(first);
+    if (e != hipSuccess || !sums) return e;
+    const dim3 grid((unsigned)a.plan.blocks, (unsigned)((a.b.features + kColumnThreads * 8 - 1) / (kColumnThreads * 8)));
+    k_columns<T, S, GATE><<<grid, dim3(kColumnThreads), 0, a.stream>>>(a);
+    e = hipGetLastError();
+    last.coef = nullptr;
+    return e == hipSuccess && over ? rows_of<T, S, 2, LN, GATE, 1024, false>(last) : e;
+  }
+  if constexpr (!LN && GATE != 2) return rows_of<T, S, 1, LN, GATE, 1024, true>(a);
+  else return a.plan.vecs == 1 ? rows_of<T, S, 1, LN, GATE, 512, true>(a) : rows_of<T, S, 2, LN, GATE, 512, true>(a);
 }
 
 }  // namespace
@@ -494,7 +679,12 @@ template <>
 hipError_t launch_backward<ZERO_NORM_DT, ZERO_NORM_S32 != 0>(const BackwardArgs& a) {
   typedef Of<ZERO_NORM_DT>::type T;
   typedef std::conditional<ZERO_NORM_S32 != 0, float, T>::type S;
-  return a.plan.vecs == 1 ? backward_of<T, S, 1>(a) : backward_of<T, S, 2>(a);
+  if (a.wide) {
+    if (a.gate_mode == 0) return backward_of<T, S, true, 0>(a);
+    return a.gate_mode == 1 ? backward_of<T, S, true, 1>(a) : backward_of<T, S, true, 2>(a);
+  }
+  if (a.gate_mode == 0) return backward_of<T, S, false, 0>(a);
+  return a.gate_mode == 1 ? backward_of<T, S, false, 1>(a) : backward_of<T, S, false, 2>(a);
 }
 
 }  // namespace norm
