@@ -238,6 +238,20 @@ def test_offsets_strides_in_place_and_accumulated(dtype, stream, off, pad):
         c.check_backward()
 
 
+@pytest.mark.parametrize("gate,per", [(None, 1), ("channel", 60), ("token", 1), ("sequence", 7)])
+@pytest.mark.parametrize("n", [8200, 12289])
+def test_wide_rows_in_place_and_accumulated(n, gate, per):
+    """Rows whose sums are formed apart read dy after the rows' own pass: dx may still be dy."""
+    c = Case(n, 60, n, "bf16", "bf16", "layer", "rms", gate, per)
+    c.forward()
+    c.backward("f32", accumulate=True)
+    c.check_backward()
+    c.backward("bf16", in_place=True)
+    c.check_backward()
+    c.backward(only=["dx", "dpre_weight"], in_place=True)
+    c.check_backward()
+
+
 def test_any_subset_of_the_gradients():
     c = Case(5, 50, 300, "bf16", "f32", "layer", "layer", "channel", 50)
     c.forward()

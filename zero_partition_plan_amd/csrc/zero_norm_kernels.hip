@@ -2,7 +2,8 @@
 // pre norm, forward and backward. Compiled once per 16-bit type (-DZERO_NORM_DT) and stream type
 // (-DZERO_NORM_S32).
 //
-// Memory is the bound (8 to 16 bytes an element forward, 12 to 20 backward). A row lies in the registers of
+// Memory is the bound (8 to 12 bytes an element forward, 12 to 18 backward; 8192 x 4096 forward with an fp32 stream and a
+// gate 75 to 78 us, 5.2 to 5.4 TB/s; backward with a 16-bit stream, a gate and two weights 91, 4.5, of which the join takes 5). A row lies in the registers of
 // its waves, 8 columns (16 bytes of a 16-bit type) a lane and vector, so every array is read once.
 //
 // Backward: with gh = dh*w_pre, base = dy + r_pre*gh, xh and oh the normalised values and
@@ -116,18 +117,32 @@ __device__ __forceinline__ void store8(T* p, int have, const float (&x)[8], bool
   }
 }
 
+// The sum of v over the first W lanes of each 16 (W a power of two), in all of them: one read of LDS for each lane and
+// moves inside the vector unit, in place of a read for each wave.
+template <int CTRL>
+__device__ __forceinline__ float plus(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+__device__ __forceinline__ float few_sum(float v, uint32_t W) {
+  if (W > 1) v = plus<0xb1>(v);   // lanes 1 apart
+  if (W > 2) v = plus<0x4e>(v);   // 2 apart
+  if (W > 4) v = plus<0x141>(v);  // the other four of eight
+  if (W > 8) v = plus<0x140>(v);  // the other eight
+  return v;
+}
+
 // A sum over the waves of a block that holds one row. `slot` alternates, so one barrier a sum is enough.
 template <int MAXW>
 __device__ __forceinline__ float row_sum(float v, float (*lds)[MAXW], int& slot) {
   v = wave_sum(v);
-  const int waves = blockDim.x / 64;
+  const uint32_t waves = blockDim.x / 64, l = threadIdx.x % 16;
   if (waves == 1) return v;
   if (threadIdx.x % 64 == 0) lds[slot][threadIdx.x / 64] = v;
   __syncthreads();
-  v = 0.0f;
-  for (int i = 0; i < waves; ++i) v += lds[slot][i];
+  v = l < waves ? lds[slot][l] : 0.0f;
   slot ^= 1;
-  return v;
+  return few_sum(v, 16);
 }
 
 // Mean and 1/deviation of a row of 8*NV columns a lane.
@@ -154,8 +169,9 @@ __device__ __forceinline__ void moments(const float (&v)[NV][8], const int (&hav
   rstd = 1.0f / sqrtf(row_sum<MAXW>(s, lds, slot) * inv_n + eps);
 }
 
-// One block a row.
-template <typename T, typename S, int NV>
+// One block a row. WHOLE: the columns are a multiple of 8; then a lane behind the row's end reads the row's start, which
+// does not count, and every load goes out without a condition before the first sum waits for one.
+template <typename T, typename S, int NV, bool WHOLE>
 __global__ __launch_bounds__(1024) void k_forward(ForwardArgs a, uint32_t gate_step, bool past) {
   __shared__ float lds[2][16];
   const zero_norm_block& b = a.b;
@@ -167,40 +183,54 @@ __global__ __launch_bounds__(1024) void k_forward(ForwardArgs a, uint32_t gate_s
   uint32_t col[NV];
   float v[NV][8];
   float mean = 0.0f, rstd = 1.0f, post_mean = 0.0f, post_rstd = 1.0f;
-  const S* x = static_cast<const S*>(a.x) + row * a.ldx;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     col[i] = (i * blockDim.x + threadIdx.x) * 8;
     have[i] = have_of(d, col[i]);
   }
+  auto load = [&](auto* p, int i) {
+    typedef typename std::remove_const<typename std::remove_pointer<decltype(p)>::type>::type E;
+    if constexpr (WHOLE) return load_all<E>(p + (have[i] ? col[i] : 0u));
+    else return load8<E>(p + (have[i] ? col[i] : 0u), have[i]);
+  };
+  const T *post_w = static_cast<const T*>(b.post_weight), *post_b = static_cast<const T*>(b.post_bias);
+  const T *pre_w = static_cast<const T*>(b.pre_weight), *pre_b = static_cast<const T*>(b.pre_bias);
+  const T* gate = b.gate ? static_cast<const T*>(b.gate) + (uint64_t)((uint32_t)row / gate_step) * b.ld_gate : nullptr;
   Eight<S> xs[NV];
+  Eight<T> os[NV], w[NV], c[NV], g[NV], u[NV], e[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) xs[i] = load8<S>(x + col[i], have[i]);
+  for (int i = 0; i < NV; ++i) {
+    if (b.branch) os[i] = load(static_cast<const T*>(b.branch) + row * b.ld_branch, i);
+    xs[i] = load(static_cast<const S*>(a.x) + row * a.ldx, i);
+  }
+  // the parameters with them, but of two vectors where they are used: 4096 x 12288 112 us, and 133 with all held
+  auto post_parameters = [&](int i) {
+    if (post_w) w[i] = load(post_w, i);
+    if (post_b) c[i] = load(post_b, i);
+    if (gate) g[i] = load(gate, i);
+  };
+  auto pre_parameters = [&](int i) {
+    if (pre_w) u[i] = load(pre_w, i);
+    if (pre_b) e[i] = load(pre_b, i);
+  };
+  if constexpr (NV == 1) post_parameters(0), pre_parameters(0);
   if (b.branch) {
-    const T* o = static_cast<const T*>(b.branch) + row * b.ld_branch;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const Eight<T> e = load8<T>(o + col[i], have[i]);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = e[j];
-    }
-    if (b.post != ZERO_NORM_NONE) {
-      moments<NV, 16>(v, have, b.post, inv_n, b.eps, lds, slot, post_mean, post_rstd);
-    }
+      for (int j = 0; j < 8; ++j) v[i][j] = j < have[i] ? os[i][j] : 0.0f;
+    if (b.post != ZERO_NORM_NONE) moments<NV, 16>(v, have, b.post, inv_n, b.eps, lds, slot, post_mean, post_rstd);
     S* y = static_cast<S*>(a.y) + row * a.ldy;
-    const T* gate = b.gate ? static_cast<const T*>(b.gate) + (uint64_t)((uint32_t)row / gate_step) * b.ld_gate : nullptr;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const Eight<T> w = b.post_weight ? load8<T>(static_cast<const T*>(b.post_weight) + col[i], have[i]) : Eight<T>{};
-      const Eight<T> c = b.post_bias ? load8<T>(static_cast<const T*>(b.post_bias) + col[i], have[i]) : Eight<T>{};
-      const Eight<T> g = gate ? load8<T>(gate + col[i], have[i]) : Eight<T>{};
+      if constexpr (NV > 1) post_parameters(i);
       float out[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float t = (v[i][j] - post_mean) * post_rstd;
-        if (b.post_weight) t = t * w[j];
-        if (b.post_bias) t = t + c[j];
-        if (gate) t = t * g[j];
+        if (post_w) t = t * w[i][j];
+        if (post_b) t = t + c[i][j];
+        if (gate) t = t * g[i][j];
         out[j] = b.residual_scale * xs[i][j] + b.branch_scale * t;
         v[i][j] = j < have[i] ? (float)(S)out[j] : 0.0f;
       }
@@ -210,21 +240,20 @@ __global__ __launch_bounds__(1024) void k_forward(ForwardArgs a, uint32_t gate_s
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = xs[i][j];
+      for (int j = 0; j < 8; ++j) v[i][j] = j < have[i] ? xs[i][j] : 0.0f;
   }
   if (b.pre != ZERO_NORM_NONE) {
     moments<NV, 16>(v, have, b.pre, inv_n, b.eps, lds, slot, mean, rstd);
     T* h = static_cast<T*>(a.h) + row * a.ldh;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const Eight<T> w = b.pre_weight ? load8<T>(static_cast<const T*>(b.pre_weight) + col[i], have[i]) : Eight<T>{};
-      const Eight<T> c = b.pre_bias ? load8<T>(static_cast<const T*>(b.pre_bias) + col[i], have[i]) : Eight<T>{};
+      if constexpr (NV > 1) pre_parameters(i);
       float out[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         out[j] = (v[i][j] - mean) * rstd;
-        if (b.pre_weight) out[j] = out[j] * w[j];
-        if (b.pre_bias) out[j] = out[j] + c[j];
+        if (pre_w) out[j] = out[j] * u[i][j];
+        if (pre_b) out[j] = out[j] + e[i][j];
       }
       store8<T>(h + col[i], have[i], out, false);
     }
@@ -413,14 +442,25 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
             *reinterpret_cast<float4*>(&lds[slot][wave][k]) = make_float4(sum[k], sum[k + 1], sum[k + 2], sum[k + 3]);
         }
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kOut; ++k) sum[k] = 0.0f;
-        for (uint32_t w = 0; w < W; ++w)
+        // a read for each wave up to 8; moves between lanes are the longer chain there (8192 x 4096 with two layer
+        // norms 113 us and 121, but 4096 x 5120 without 73 and 65)
+        if (NT > 512 && W > 8) {
 #pragma unroll
           for (int k = 0; k < kOut; k += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&lds[slot][group * W + w][k]);
-            sum[k] += o.x, sum[k + 1] += o.y, sum[k + 2] += o.z, sum[k + 3] += o.w;
+            const float4 o = *reinterpret_cast<const float4*>(&lds[slot][group * W + threadIdx.x % W][k]);
+            sum[k] = few_sum(o.x, W), sum[k + 1] = few_sum(o.y, W), sum[k + 2] = few_sum(o.z, W);
+            sum[k + 3] = few_sum(o.w, W);
           }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kOut; ++k) sum[k] = 0.0f;
+          for (uint32_t w = 0; w < W; ++w)
+#pragma unroll
+            for (int k = 0; k < kOut; k += 4) {
+              const float4 o = *reinterpret_cast<const float4*>(&lds[slot][group * W + w][k]);
+              sum[k] += o.x, sum[k + 1] += o.y, sum[k + 2] += o.z, sum[k + 3] += o.w;
+            }
+        }
         slot ^= 1;
       }
       const float c1 = sum[0] * inv_n, m1 = LN && b.pre == ZERO_NORM_LAYER ? sum[3] * inv_n : 0.0f;
@@ -536,7 +576,7 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
 
 // The sums over rows where a row takes so many registers that k_backward cannot hold them beside it: each thread
 // walks its 8 columns down the block's rows, with each row's m1 and c1 from k_backward, and reads the arrays
-// again (4096 x 12288 with an fp32 stream and a layer norm ZERO_MEASURED us; held in one kernel, and so partly in
+// again (4096 x 12288 with an fp32 stream and a layer norm 282 us; held in one kernel, and so partly in
 // memory, 735).
 constexpr int kColumnThreads = 256;
 
@@ -665,12 +705,15 @@ hipError_t launch_forward<ZERO_NORM_DT, ZERO_NORM_S32 != 0>(const ForwardArgs& a
   const dim3 grid((unsigned)wide, (unsigned)((a.b.rows + wide - 1) / wide));
   const uint32_t step = a.b.gate ? (uint32_t)(a.b.gate_rows < a.b.rows ? a.b.gate_rows : a.b.rows) : 1u;
   const bool past = a.b.rows * a.b.features * sizeof(S) >= (128ull << 20);
+  const bool whole = a.b.features % 8 == 0;
   if (vecs <= 1024) {
     const dim3 block((unsigned)((vecs + 63) / 64 * 64));
-    k_forward<T, S, 1><<<grid, block, 0, a.stream>>>(a, step, past);
+    if (whole) k_forward<T, S, 1, true><<<grid, block, 0, a.stream>>>(a, step, past);
+    else k_forward<T, S, 1, false><<<grid, block, 0, a.stream>>>(a, step, past);
   } else {
     const dim3 block((unsigned)(((vecs + 1) / 2 + 63) / 64 * 64));
-    k_forward<T, S, 2><<<grid, block, 0, a.stream>>>(a, step, past);
+    if (whole) k_forward<T, S, 2, true><<<grid, block, 0, a.stream>>>(a, step, past);
+    else k_forward<T, S, 2, false><<<grid, block, 0, a.stream>>>(a, step, past);
   }
   return hipGetLastError();
 }
