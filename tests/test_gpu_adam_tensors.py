@@ -317,3 +317,21 @@ def test_two_streams_and_another_device_refused():
         Z.zero_adam_tensors_step([_entry(dev[0]), Z.adam_tensor(*(torch.zeros(8, device=DEV) for _ in range(4)))],
                                  Z.adam_hparams())
     Z.zero_adam_tensors_step([], Z.adam_hparams())
+
+
+def test_a_gradient_shared_by_tensors_and_a_stream_given():
+    rng = np.random.default_rng(29)
+    t = _host_tensor(rng, 3001, 8, "bf16")
+    d, e = _place(t, 8, "bf16", "bf16", 0), _place(t, 8, "bf16", "f16", 1)
+    e["out"] = _place(t, 8, "bf16", "bf16", 1)["out"]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    one = Z.adam_tensor(d["p"].t, d["g"].t, d["m"].t, d["v"].t, out=d["out"].t, m_scale=d["ms"].t, v_scale=d["vs"].t)
+    two = Z.adam_tensor(e["p"].t, d["g"].t, e["m"].t, e["v"].t, out=e["out"].t, m_scale=e["ms"].t, v_scale=e["vs"].t)
+    Z.zero_adam_tensors_step([one, two], Z.adam_hparams(**HP), stream=side)
+    side.synchronize()
+    want = _want(t, 8, "bf16", 1.0, O.AdamHParams(**HP), "bf16")
+    _check(d, want, 8, "bf16", "first")
+    _check(e, want, 8, "bf16", "second")
+    with pytest.raises(Z.ZeroError):
+        Z.zero_adam_tensors_step([one, one], Z.adam_hparams(**HP))

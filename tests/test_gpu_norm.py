@@ -381,3 +381,50 @@ def test_streams_past_32_bits():
     Z.zero_norm_backward(y2, s2, dy=x[tail], dh=dh[tail], branch=o[tail], post="rms", dx=dx2, dbranch=do2)
     torch.cuda.synchronize()
     assert torch.equal(dx[tail], dx2) and torch.equal(do[tail], do2)
+
+
+def test_more_rows_than_one_grid_dimension_holds():
+    R, n = (1 << 20) + 37, 40
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    x, o, dy, dh = (torch.empty(R, n, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(4))
+    gate = torch.empty(-(-R // 1000), n, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    kw = dict(branch=o, gate=gate, gate_rows=1000, post="rms", pre="layer")
+    y, h, st = torch.empty_like(x), torch.empty_like(x), torch.empty(R, 4, device=DEV)
+    Z.zero_norm_forward(x, h=h, y=y, stats=st, **kw)
+    dx, do, dg = torch.empty_like(x), torch.empty_like(x), torch.empty(gate.shape, device=DEV)
+    ws = torch.empty(Z.zero_norm_workspace_bytes(R, n, gate_rows=1000), dtype=torch.uint8, device=DEV)
+    Z.zero_norm_backward(y, st, dy=dy, dh=dh, dx=dx, dbranch=do, dgate=dg, workspace=ws, **kw)
+    first = R // 1000 * 1000                                # the last gate's rows, alone
+    t = slice(first, R)
+    kw.update(branch=o[t], gate=gate[first // 1000:])
+    y2, h2, st2 = torch.empty_like(x[t]), torch.empty_like(x[t]), torch.empty(R - first, 4, device=DEV)
+    Z.zero_norm_forward(x[t], h=h2, y=y2, stats=st2, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(y[t], y2) and torch.equal(h[t], h2) and torch.equal(st[t], st2)
+    dx2, do2, dg2 = torch.empty_like(y2), torch.empty_like(y2), torch.empty(1, n, device=DEV)
+    Z.zero_norm_backward(y2, st2, dy=dy[t], dh=dh[t], dx=dx2, dbranch=do2, dgate=dg2, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(dx[t], dx2) and torch.equal(do[t], do2)
+    # sums of up to 48 rows in another order: 48 u of their magnitudes
+    xh, _, _ = N.normalised(host(o[t]), "rms", 1e-5)
+    size = (np.abs(host(dx2)) * (np.abs(xh) + 1)).sum(0)
+    close(host(dg)[-1], host(dg2)[0], (K + 64 * U) * size, "dgate")
+
+
+def test_columns_of_one_buffer_and_a_stream_given():
+    """Slices of one buffer's columns do not overlap; work goes to the stream that is given."""
+    c = Case(13, 30, 64, "bf16", "bf16", "rms", "rms")
+    y, h = (t.clone() for t in c.forward())
+    buf = torch.zeros(30, 4 * 64, dtype=torch.bfloat16, device=DEV)
+    x, o, y2, h2 = buf.split(64, 1)
+    x.copy_(c.x)
+    o.copy_(c.branch)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    kw = {**c.kw(), "branch": o}
+    Z.zero_norm_forward(x, h=h2, y=y2, stream=side, **kw)
+    side.synchronize()
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    with pytest.raises(Z.ZeroError):
+        Z.zero_norm_forward(x, h=buf[:, 96:160], y=y2, **kw)     # half in the branch, half in y

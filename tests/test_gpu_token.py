@@ -444,3 +444,34 @@ def test_logits_past_32_bits():
     Z.zero_policy_step(z[tail], label[tail], old[tail], adv[tail], loss2, grad2)
     torch.cuda.synchronize()
     assert torch.equal(loss[tail], loss2) and torch.equal(grad[tail], grad2)
+
+
+def test_more_rows_than_one_grid_dimension_holds():
+    R, V = (1 << 21) + 5, 9
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    z = torch.empty(R, V, device=DEV).normal_(generator=g)
+    label = torch.randint(-1, V, (R,), generator=g, device=DEV, dtype=torch.int32)
+    old, adv = torch.empty(R, device=DEV).normal_(-2, 0.3, generator=g), torch.empty(R, device=DEV).normal_(generator=g)
+    loss, logp, grad = torch.empty(R, device=DEV), torch.empty(R, device=DEV), torch.empty_like(z)
+    Z.zero_policy_step(z, label, old, adv, loss, grad, logp=logp)
+    stats, grad2 = torch.empty(R, Z.ZERO_TOKEN_STATS, device=DEV), torch.empty_like(z)
+    start = torch.tensor([0, R // 2, R], device=DEV)
+    pair = torch.empty(1, device=DEV)
+    Z.zero_preference_forward(z, label, start, pair, stats, average=True)
+    Z.zero_token_backward(z, label, stats, grad2)
+    torch.cuda.synchronize()
+    l = torch.log_softmax(z.double(), 1)
+    on = label >= 0
+    want = torch.where(on, l.gather(1, label.long().clamp(min=0)[:, None])[:, 0], torch.zeros(R, dtype=torch.float64, device=DEV))
+    rel = (V / 256 + 16 + 4 * 30) * U
+    assert float((logp.double() - want).abs().max()) <= rel + 2 * U * float(want.abs().max())
+    assert bool((grad[~on] == 0).all()) and bool((loss[~on] == 0).all())
+    means = [float(want[a:b].sum() / max(1, int(on[a:b].sum()))) for a, b in ((0, R // 2), (R // 2, R))]
+    x = 0.1 * (means[0] - means[1])
+    assert abs(float(pair) - np.logaddexp(0, -x)) <= 0.2 * rel + 4 * U
+    s = -0.1 / (1 + np.exp(x)) / int(on[:R // 2].sum())
+    first = int(torch.nonzero(on)[0])
+    q = l[first].exp()
+    q[int(label[first])] -= 1
+    assert float((grad2[first].double() + s * q).abs().max()) <= abs(s) * (rel + 0.2 * rel + 16 * U)
