@@ -16,6 +16,15 @@ import zero_partition_plan_amd as Z
 from gpu_util import DEV, banner
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _memory_given_back():
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
 N = O.norm
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}

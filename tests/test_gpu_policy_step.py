@@ -11,6 +11,15 @@ from block_chain import BlockChain
 from gpu_util import DEV, assert_bits_equal, banner, bits16, bits32
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _memory_given_back():
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
 NAMES = {torch.float16: "f16", torch.bfloat16: "bf16"}
 
 

@@ -10,6 +10,15 @@ import zero_partition_plan_amd as Z
 from gpu_util import DEV, assert_bits_equal, assert_bits_equal_nan, banner
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _memory_given_back():
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
 T16 = {"bf16": torch.bfloat16, "f16": torch.float16}
 DT = {**T16, "f32": torch.float32}
 HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=5)
