@@ -50,16 +50,22 @@ struct Args {
 enum { kForward = 1, kBackward = 2, kStep = 3 };  // bit 0: loss, bit 1: gradient
 
 // A place on the base-2 scale that exponentials are taken from: 2^(z c - k) is 2^((z - m) c) up to a factor that is
-// the same for every z, k being m c rounded, and z c - k is one fused operation. c is one fp32 number there, which
-// takes up to 2^-26 of (m - z) c off an exponent; where it would be more (by the temperature), and where m c
-// nears fp32's end (a row of the type's lowest numbers), k is infinite and differences are formed first.
+// the same for every z, k being m c rounded, and z c - k is one fused operation. The factor's exponent is what the
+// rounding took: at most 1/2 for |k| up to 2^24, so it is used there. Further out (a row masked by -1e10, say, where it
+// would pass fp32's range) k is infinite and differences are formed first; and so where c needs two fp32 numbers, as one
+// takes up to 2^-26 of (m - z) c off an exponent, and more by the temperature.
 struct From {
   float m, k;
 };
 
 __device__ __forceinline__ From from(const Args& a, float m) {
   const float k = m * a.c_hi;
-  return From{m, !a.two && fabsf(k) < 1e37f ? k : INFINITY};
+  return From{m, !a.two && fabsf(k) <= 0x1p24f ? k : INFINITY};
+}
+
+// m c - k: what a place's rounding took
+__device__ __forceinline__ float rounded_off(const Args& a, From f) {
+  return f.k < INFINITY ? __builtin_fmaf(f.m, a.c_hi, -f.k) : 0.0f;
 }
 
 // c * d to fp32 accuracy. -inf is taken as the lowest finite number (c_lo may be negative or 0, and would
@@ -89,7 +95,8 @@ __device__ __forceinline__ float exponential(const Args& a, From f, float z) {
 
 // What a sum counted from `f` is multiplied by to count from `to`.
 __device__ __forceinline__ float moved_to(const Args& a, From f, From to) {
-  return f.k < INFINITY && to.k < INFINITY ? ex2(f.k - to.k) : ex2(mul_c(a, f.m - to.m));
+  if (f.k < INFINITY && to.k < INFINITY) return ex2(f.k - to.k);
+  return ex2(mul_c(a, f.m - to.m) - rounded_off(a, f) + rounded_off(a, to));
 }
 
 // A sum of exponentials and the place it counts from, one of the numbers seen. Starts at the lowest finite
