@@ -125,3 +125,25 @@ def test_a_token_alone_is_certain_at_any_temperature(V, dtype, T):
     Z.zero_policy_step(z, label, torch.zeros(3, device=DEV), adv, loss, grad, temperature=T, logp=logp)
     torch.cuda.synchronize()
     assert bool((logp == 0).all()) and bool((grad == 0).all()) and torch.equal(loss, -adv)
+
+
+@pytest.mark.parametrize("kind", ["step", "calls"])
+def test_a_token_without_mass_is_infinitely_far_from_a_reference(kind):
+    """l = -inf with a finite reference: the KL term is inf, the derivative in l -inf; the reference's -inf with a finite l
+    gives inf too, and the derivative kl."""
+    V, kl = 9, 0.25
+    z = torch.zeros(6, V, device=DEV)
+    z[:3, 3] = float("-inf")
+    s = dict(logits=z, label=torch.full((6,), 3, device=DEV), old=torch.full((6,), -2.0, device=DEV),
+             ref=torch.tensor([0.0, -1.0, -60.0] + [float("-inf")] * 3, device=DEV),
+             adv=torch.tensor([1.0, -1.0, 0.0] * 2, device=DEV), weight=torch.ones(6, device=DEV),
+             upstream=torch.ones(6, device=DEV))
+    loss, logp, grad = G.run(s, kind, clip=(0.2, 0.2), kl=kl, scale=1.0)
+    assert (loss == np.inf).all()
+    assert (logp[:3] == -np.inf).all() and np.abs(logp[3:] + np.log(V)).max() <= 32 * G.U
+    token = np.arange(V) == 3
+    assert (grad[:3, token] == -np.inf).all() and (grad[:3, ~token] == np.inf).all()
+    l = -np.log(V)
+    slope = np.array([O.token.policy(l, -2.0, a, (0.2, 0.2))[1] for a in (1.0, -1.0, 0.0)]) + kl
+    want = slope[:, None] * (token - 1.0 / V)
+    assert np.abs(grad[3:] - want).max() <= 64 * G.U

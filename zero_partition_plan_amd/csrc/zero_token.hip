@@ -136,9 +136,12 @@ __device__ __forceinline__ void add(const Args& a, PlaceSum& r, float (&z)[N], u
   r.s = s;
 }
 
-// exp(d) - 1 - d without the digits that cancel near 0
+// exp(d) - 1 - d without the digits that cancel near 0; inf for either infinite d
 __device__ __forceinline__ float kl_term(float d) {
-  if (!(fabsf(d) < 0.5f)) return expm1f(d) - d;
+  if (!(fabsf(d) < 0.5f)) {
+    const float e = expm1f(d);
+    return e == INFINITY ? e : e - d;
+  }
   float s = 1.0f;
 #pragma unroll
   for (int k = 9; k >= 3; --k) s = 1.0f + d * (1.0f / (float)k) * s;
