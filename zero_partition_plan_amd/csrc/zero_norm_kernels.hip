@@ -475,7 +475,7 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
         Held<T, S, GATE>& r = held[i];
         again(r.y), again(r.dy), again(r.dh), again(r.o);
         if constexpr (GATE == 2) again(r.g);
-        float dx[8], db[8], dg[8];
+        float dx[8], db[8], dg[8], oh[8];
         Eight<T> bias{};
         if (GATE == 2 && a.dgate && b.post_bias) bias = load8<T>(static_cast<const T*>(b.post_bias) + (have[i] ? col[i] : 0u), have[i]);
 #pragma unroll
@@ -483,24 +483,28 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
           const float dh = r.dh[j];
           const float xh = (r.y[j] - mp) * rp;
           const float D = r.dy[j] + rp * (dh * wpre[i][j]) - rp * (m1 + xh * c1);
-          const float oh = (r.o[j] - mo) * ro;
+          oh[j] = (r.o[j] - mo) * ro;
           float e = D;
           if constexpr (GATE == 2) {
-            dg[j] = b.branch_scale * D * (oh * wpost[i][j] + bias[j]);
+            dg[j] = b.branch_scale * D * (oh[j] * wpost[i][j] + bias[j]);
             e *= r.g[j];
           }
           float u = b.branch_scale * e * wpost[i][j];
           if constexpr (GATE == 1) u *= gate[i][j];
           dx[j] = scale * D;
-          db[j] = ro * (u - m2 - oh * c2);
+          db[j] = u;
           if constexpr (SUMS) {
             s_xh[i][j] += dh * xh;
-            s_oh[i][j] += e * oh;
+            s_oh[i][j] += e * oh[j];
           }
           if constexpr (SUMS && LN) {
             s_dh[i][j] += dh;
             s_e[i][j] += e;
           }
+        }
+        if (post) {  // without a norm the branch has no part in its own gradient, an inf of it neither
+#pragma unroll
+          for (int j = 0; j < 8; ++j) db[j] = ro * (db[j] - m2 - oh[j] * c2);
         }
         if (a.dx) store8<S>(static_cast<S*>(a.dx) + row * a.lddx + col[i], have[i], dx, false);
         if (a.dbranch) store8<T>(static_cast<T*>(a.dbranch) + row * a.lddbranch + col[i], have[i], db, false);
