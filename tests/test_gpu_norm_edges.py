@@ -1,4 +1,4 @@
-"""GPU parity of the block boundaries where single entries are infinite or NaN.
+"""GPU parity of the block boundaries where single entries are infinite or NaN, and of statistics off 16 bytes.
 Bounds: those of test_gpu_norm."""
 
 import numpy as np
@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import test_gpu_norm as G
-from gpu_util import banner
+import zero_partition_plan_amd as Z
+from gpu_util import DEV, banner
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,25 @@ def test_a_branch_without_a_norm_has_no_part_in_its_own_gradient(dtype, stream, 
         size = np.zeros((len(c.gate), n))
         np.add.at(size, np.arange(6) // per, np.abs(each))
         G.close(G.host(c.grads["dgate"]), want, (G.K + 6 * G.U) * size, "dgate")
+
+
+@pytest.mark.parametrize("n", [96, 4096, 8208])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_statistics_at_any_float(off, n):
+    """stats is an array of float: every multiple of 4 bytes is a place for it."""
+    c = G.Case(off, 9, n, "bf16", "bf16", "layer", "rms", "channel", 9)
+    y, h = (t.clone() for t in c.forward())
+    first = c.backward()
+    buf = torch.full((4 * 9 + 8,), -7.0, device=DEV)
+    stats = buf[off:off + 36].view(9, 4)
+    y2, h2 = torch.empty_like(y), torch.empty_like(h)
+    Z.zero_norm_forward(c.x, h=h2, y=y2, stats=stats, **c.kw())
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(stats, c.stats)
+    assert bool((buf[:off] == -7.0).all()) and bool((buf[off + 36:] == -7.0).all())
+    grads = {k: torch.empty_like(t) for k, t in c.grads.items()}
+    ws = torch.empty(Z.zero_norm_workspace_bytes(9, n, gate_rows=9), dtype=torch.uint8, device=DEV)
+    Z.zero_norm_backward(c.y, stats, dy=c.dy, dh=c.dh, workspace=ws, **grads, **c.kw())
+    torch.cuda.synchronize()
+    for k, t in grads.items():
+        assert np.array_equal(G.host(t), first[k]), k

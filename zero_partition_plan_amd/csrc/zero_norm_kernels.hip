@@ -52,6 +52,9 @@ struct Eight<float> {
   __device__ __forceinline__ float operator[](int j) const { return v[j / 4][j % 4]; }
 };
 
+// A row's statistics, which may lie at any multiple of 4 bytes.
+typedef float Stats __attribute__((ext_vector_type(4), aligned(4)));
+
 // Columns that exist behind column c of d: 8 but at a row's end.
 __device__ __forceinline__ int have_of(uint32_t d, uint32_t c) { return c + 8 <= d ? 8 : c < d ? (int)(d - c) : 0; }
 
@@ -259,7 +262,7 @@ __global__ __launch_bounds__(1024) void k_forward(ForwardArgs a, uint32_t gate_s
     }
   }
   if (a.stats && threadIdx.x == 0)
-    *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(post_mean, post_rstd, mean, rstd);
+    *reinterpret_cast<Stats*>(a.stats + 4 * row) = Stats{post_mean, post_rstd, mean, rstd};
 }
 
 // Keeps what is computed from x from being formed earlier and held in registers.
@@ -390,11 +393,11 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
     };
     // the next row's arrays are asked for before this one's are used, where the registers hold both
     Held<T, S, GATE> ahead[NV];
-    float4 st_ahead;
+    Stats st_ahead;
     auto look = [&](uint64_t row) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) ahead[i] = load(row, i);
-      st_ahead = *reinterpret_cast<const float4*>(a.stats + 4 * (row < end ? row : end - 1));
+      st_ahead = *reinterpret_cast<const Stats*>(a.stats + 4 * (row < end ? row : end - 1));
     };
     if (SUMS && first < end) look(first + group);
     for (uint64_t base_row = first; base_row < end; base_row += groups) {
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
       Held<T, S, GATE> held[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) held[i] = ahead[i];
-      const float4 st = st_ahead;
+      const Stats st = st_ahead;
       if (SUMS && base_row + groups < end) look(row + groups);
       const float mo = post ? st.x : 0.0f, ro = post ? st.y : 1.0f;
       const float mp = pre ? st.z : 0.0f, rp = pre ? st.w : 0.0f;
@@ -606,7 +609,7 @@ __global__ __launch_bounds__(kColumnThreads) void k_columns(BackwardArgs a) {
     float s_oh[8] = {}, s_e[8] = {};
 #pragma unroll 2
     for (uint64_t row = first; row < end; ++row) {
-      const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * row);
+      const Stats st = *reinterpret_cast<const Stats*>(a.stats + 4 * row);
       const float mo = post ? st.x : 0.0f, ro = post ? st.y : 1.0f;
       const float mp = pre ? st.z : 0.0f, rp = pre ? st.w : 0.0f;
       Eight<S> y{}, dy{};
