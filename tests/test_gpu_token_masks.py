@@ -147,3 +147,27 @@ def test_a_token_without_mass_is_infinitely_far_from_a_reference(kind):
     slope = np.array([O.token.policy(l, -2.0, a, (0.2, 0.2))[1] for a in (1.0, -1.0, 0.0)]) + kl
     want = slope[:, None] * (token - 1.0 / V)
     assert np.abs(grad[3:] - want).max() <= 64 * G.U
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_gradient_beside_its_logits(dtype):
+    """Columns of one buffer do not overlap: the gradient may lie in other columns of the logits' rows."""
+    s = G.case(31, 6, 300, dtype)
+    buf = torch.full((7, 2 * 300 + 7), -9.0, dtype=G.DT[dtype], device=DEV)
+    z, d = buf[:6, :300], buf[:6, 304:604]
+    z.copy_(s["logits"])
+    want = G.run(s, "step")
+    loss, logp, stats = torch.empty(6, device=DEV), torch.empty(6, device=DEV), torch.empty(6, Z.ZERO_TOKEN_STATS, device=DEV)
+    kw = dict(ref_logp=s["ref"], weight=s["weight"], clip=(0.2, 0.3), kl_coef=0.1, logp=logp)
+    Z.zero_policy_step(z, s["label"], s["old"], s["adv"], loss, d, upstream=s["upstream"], scale=3.0, **kw)
+    torch.cuda.synchronize()
+    assert all(np.array_equal(G.host(a), b) for a, b in zip((loss, logp, d), want))
+    d.fill_(-9.0)
+    Z.zero_policy_forward(z, s["label"], s["old"], s["adv"], loss, stats, **kw)
+    Z.zero_token_backward(z, s["label"], stats, d, upstream=s["upstream"], scale=3.0)
+    torch.cuda.synchronize()
+    assert np.array_equal(G.host(d), G.run(s, "calls")[2])
+    assert bool((buf[:, 300:304] == -9.0).all()) and bool((buf[:, 604:] == -9.0).all())
+    for bad in (buf[:6, 299:599], buf[:6, 1:301], buf[1:, 299:599], buf.as_strided((6, 300), (607, 1), 308)):
+        with pytest.raises(Z.ZeroError):
+            Z.zero_token_backward(z, s["label"], stats, bad)

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "zero_arrays.h"
 #include "zero_norm.h"
 
 namespace zero {
@@ -98,44 +99,6 @@ uint64_t part_bytes(const Plan& p, uint64_t features) { return (p.blocks * featu
 // What k_columns needs of each row, behind the parts.
 uint64_t coef_bytes(uint64_t rows, uint64_t features) { return features > 8192 ? (rows * 8 + 15) & ~15ull : 0; }
 
-struct Arr {
-  const char* name;
-  const void* p;
-  uint64_t rows, cols, ld;
-  uint32_t bytes;  // of an element
-  bool written;
-  uint64_t size() const { return rows && cols ? ((rows - 1) * ld + cols) * bytes : 0; }
-};
-
-zero_status check_arrays(const char* fn, const Arr* arr, int n, int x0, int y0) {
-  for (int i = 0; i < n; ++i) {
-    const Arr& a = arr[i];
-    if (!a.p) continue;
-    if (a.rows > 1 && a.ld < a.cols) return fail(ZERO_E_INVAL, "%s: %s: a leading dimension below the columns", fn, a.name);
-    if (a.rows && a.ld >= (1ull << 63) / 4 / a.rows)
-      return fail(ZERO_E_OVERFLOW, "%s: %s: a byte count does not fit in 63 bits", fn, a.name);
-    if (a.size() && reinterpret_cast<uintptr_t>(a.p) % a.bytes)
-      return fail(ZERO_E_INVAL, "%s: %s is not aligned to its element size", fn, a.name);
-  }
-  // Column slices of one buffer with the same leading dimension do not overlap, though their ranges do.
-  auto apart = [](const Arr& x, const Arr& y) {
-    const uint64_t lb = x.ld * x.bytes;
-    if (x.rows < 2 || y.rows < 2 || lb != y.ld * y.bytes) return false;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(x.p), q = reinterpret_cast<uintptr_t>(y.p);
-    const uint64_t gap = p < q ? (q - p) % lb : (p - q) % lb;  // of the one behind, from the other's rows
-    const uint64_t front = (p < q ? x.cols * x.bytes : y.cols * y.bytes), back = (p < q ? y.cols * y.bytes : x.cols * x.bytes);
-    return gap >= front && gap + back <= lb;
-  };
-  for (int i = 0; i < n; ++i)
-    for (int j = 0; j < n; ++j) {
-      if (!arr[i].written || i == j || !arr[i].p || !arr[j].p) continue;
-      if (i == x0 && j == y0 && arr[i].p == arr[j].p && (arr[i].ld == arr[j].ld || arr[i].rows < 2)) continue;
-      if (overlaps(arr[i].p, arr[i].size(), arr[j].p, arr[j].size()) && !apart(arr[i], arr[j]))
-        return fail(ZERO_E_INVAL, "%s: %s overlaps %s", fn, arr[i].name, arr[j].name);
-    }
-  return ZERO_OK;
-}
-
 uint64_t gates_of(const zero_norm_block* b) {
   return b->rows / b->gate_rows + (b->rows % b->gate_rows != 0);
 }
@@ -188,6 +151,8 @@ zero_status launched(const char* fn, hipError_t e) {
 }  // namespace zero
 
 using namespace zero::norm;
+using zero::Arr;
+using zero::check_arrays;
 
 extern "C" {
 

@@ -16,6 +16,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "zero_arrays.h"
 #include "zero_internal.h"
 #include "zero_rows.h"
 
@@ -557,29 +558,6 @@ hipError_t launch_dtype(const Args& a, int mode, hipStream_t s) {
   }
 }
 
-struct Arr {
-  const char* name;
-  const void* p;
-  uint64_t bytes;
-  uint32_t align;
-  bool written;
-};
-
-// Alignment of every array and overlaps of the written ones; in_place: arr[x] may be arr[y].
-zero_status check_arrays(const char* fn, const Arr* arr, int n, int x0 = -1, int y0 = -1) {
-  for (int i = 0; i < n; ++i)
-    if (arr[i].p && arr[i].bytes && reinterpret_cast<uintptr_t>(arr[i].p) % arr[i].align)
-      return fail(ZERO_E_INVAL, "%s: %s is not aligned to its element size", fn, arr[i].name);
-  for (int i = 0; i < n; ++i)
-    for (int j = 0; j < n; ++j) {
-      if (!arr[i].written || i == j || !arr[i].p || !arr[j].p) continue;
-      if (i == x0 && j == y0 && arr[i].p == arr[j].p) continue;
-      if (overlaps(arr[i].p, arr[i].bytes, arr[j].p, arr[j].bytes))
-        return fail(ZERO_E_INVAL, "%s: %s overlaps %s", fn, arr[i].name, arr[j].name);
-    }
-  return ZERO_OK;
-}
-
 // The inputs' own checks (no arrays), and what of `a` they give.
 zero_status check_in(const char* fn, const zero_token_in* in, Args& a) {
   if (!in) return fail(ZERO_E_INVAL, "%s: in is NULL", fn);
@@ -620,9 +598,20 @@ zero_status check_policy(const char* fn, const zero_policy* p, uint64_t rows, Ar
   return ZERO_OK;
 }
 
-uint64_t logit_bytes(const Args& a, uint64_t ld) {
-  return ((a.in.rows - 1) * ld + a.in.vocab) * dtype_bytes(a.in.logit_dtype);
+// The arrays of a call, as check_arrays takes them.
+Arr logits_of(const Args& a) {
+  return Arr{"logits", a.in.logits, a.in.rows, a.in.vocab, a.in.ld_logits, dtype_bytes(a.in.logit_dtype), false};
 }
+
+Arr dlogits_of(const Args& a) {
+  return Arr{"dlogits", a.dlogits, a.in.rows, a.in.vocab, a.ldg, dtype_bytes(a.in.logit_dtype), true};
+}
+
+Arr label_of(const Args& a) {
+  return Arr{"label", a.in.label, 1, a.in.rows, a.in.rows, (uint32_t)a.in.label_bytes, false};
+}
+
+Arr floats(const char* name, const float* p, uint64_t n, bool written) { return Arr{name, p, 1, n, n, 4, written}; }
 
 zero_status check_dlogits(const char* fn, Args& a, void* dlogits, uint64_t ldg) {
   if (a.in.rows && !dlogits) return fail(ZERO_E_INVAL, "%s: NULL argument", fn);
@@ -651,20 +640,18 @@ zero_status policy(const char* fn, const zero_token_in* in, const zero_policy* p
   if (in->rows == 0) return ok();
   if (!loss || (mode == kForward && !stats)) return fail(ZERO_E_INVAL, "%s: NULL argument", fn);
   const uint64_t R = in->rows;
-  const uint32_t e = dtype_bytes(in->logit_dtype);
-  const Arr arr[] = {{"logits", in->logits, logit_bytes(a, a.in.ld_logits), e, false},
-                     {"dlogits", mode == kStep ? dlogits : nullptr, mode == kStep ? logit_bytes(a, a.ldg) : 0, e, true},
-                     {"label", in->label, R * in->label_bytes, (uint32_t)in->label_bytes, false},
-                     {"old_logp", p->old_logp, R * 4, 4, false},
-                     {"advantage", p->advantage, R * 4, 4, false},
-                     {"ref_logp", p->ref_logp, R * 4, 4, false},
-                     {"weight", p->weight, R * 4, 4, false},
-                     {"upstream", upstream, R * 4, 4, false},
-                     {"loss", loss, R * 4, 4, true},
-                     {"logp", logp, R * 4, 4, true},
-                     {"stats", stats, R * ZERO_TOKEN_STATS * 4, 4, true}};
-  const bool in_place = mode == kStep && a.ldg == a.in.ld_logits;
-  st = check_arrays(fn, arr, sizeof(arr) / sizeof(arr[0]), in_place ? 1 : -1, 0);
+  const Arr arr[] = {logits_of(a),
+                     dlogits_of(a),
+                     label_of(a),
+                     floats("old_logp", p->old_logp, R, false),
+                     floats("advantage", p->advantage, R, false),
+                     floats("ref_logp", p->ref_logp, R, false),
+                     floats("weight", p->weight, R, false),
+                     floats("upstream", upstream, R, false),
+                     floats("loss", loss, R, true),
+                     floats("logp", logp, R, true),
+                     floats("stats", stats, R * ZERO_TOKEN_STATS, true)};
+  st = check_arrays(fn, arr, sizeof(arr) / sizeof(arr[0]), 1, 0);
   if (st != ZERO_OK) return st;
   a.upstream = upstream;
   a.n_up = R;
@@ -689,11 +676,8 @@ zero_status zero_token_logp(const zero_token_in* in, float* logp, float* stats, 
   if (in->rows == 0) return zero::ok();
   if (!logp) return zero::fail(ZERO_E_INVAL, "%s: NULL argument", fn);
   const uint64_t R = in->rows;
-  const zero::Arr arr[] = {
-      {"logits", in->logits, zero::logit_bytes(a, a.in.ld_logits), zero::dtype_bytes(in->logit_dtype), false},
-      {"label", in->label, R * in->label_bytes, (uint32_t)in->label_bytes, false},
-      {"logp", logp, R * 4, 4, true},
-      {"stats", stats, R * ZERO_TOKEN_STATS * 4, 4, true}};
+  const zero::Arr arr[] = {zero::logits_of(a), zero::label_of(a), zero::floats("logp", logp, R, true),
+                           zero::floats("stats", stats, R * ZERO_TOKEN_STATS, true)};
   st = zero::check_arrays(fn, arr, 4);
   if (st != ZERO_OK) return st;
   a.logp = logp;
@@ -728,16 +712,16 @@ zero_status zero_preference_forward(const zero_token_in* in, const zero_preferen
   if ((p->pairs && (!p->seq_start || !loss)) || (in->rows && !stats))
     return zero::fail(ZERO_E_INVAL, "%s: NULL argument", fn);
   const uint64_t R = in->rows, P = p->pairs;
-  const zero::Arr arr[] = {
-      {"logits", in->logits, R ? zero::logit_bytes(a, a.in.ld_logits) : 0, zero::dtype_bytes(in->logit_dtype), false},
-      {"label", in->label, R * in->label_bytes, (uint32_t)in->label_bytes, false},
-      {"seq_start", p->seq_start, P ? (2 * P + 1) * p->start_bytes : 0, (uint32_t)p->start_bytes, false},
-      {"ref_logp", p->ref_logp, 2 * P * 4, 4, false},
-      {"weight", p->weight, P * 4, 4, false},
-      {"loss", loss, P * 4, 4, true},
-      {"logp", logp, R * 4, 4, true},
-      {"seq_logp", seq_logp, 2 * P * 4, 4, true},
-      {"stats", stats, R * ZERO_TOKEN_STATS * 4, 4, true}};
+  const uint64_t starts = P ? 2 * P + 1 : 0;
+  const zero::Arr arr[] = {zero::logits_of(a),
+                           zero::label_of(a),
+                           {"seq_start", p->seq_start, 1, starts, starts, (uint32_t)p->start_bytes, false},
+                           zero::floats("ref_logp", p->ref_logp, 2 * P, false),
+                           zero::floats("weight", p->weight, P, false),
+                           zero::floats("loss", loss, P, true),
+                           zero::floats("logp", logp, R, true),
+                           zero::floats("seq_logp", seq_logp, 2 * P, true),
+                           zero::floats("stats", stats, R * ZERO_TOKEN_STATS, true)};
   st = zero::check_arrays(fn, arr, sizeof(arr) / sizeof(arr[0]));
   if (st != ZERO_OK) return st;
   if (R == 0 && P == 0) return zero::ok();
@@ -769,14 +753,10 @@ zero_status zero_token_backward(const zero_token_in* in, const float* stats, con
   if (!stats) return zero::fail(ZERO_E_INVAL, "%s: NULL argument", fn);
   if (n_upstream > zero::kMaxSize) return zero::fail(ZERO_E_OVERFLOW, "%s: n_upstream above 2^31 - 1", fn);
   const uint64_t R = in->rows;
-  const uint32_t eb = zero::dtype_bytes(in->logit_dtype);
-  const zero::Arr arr[] = {
-      {"logits", in->logits, zero::logit_bytes(a, a.in.ld_logits), eb, false},
-      {"dlogits", dlogits, zero::logit_bytes(a, a.ldg), eb, true},
-      {"label", in->label, R * in->label_bytes, (uint32_t)in->label_bytes, false},
-      {"stats", stats, R * ZERO_TOKEN_STATS * 4, 4, false},
-      {"upstream", upstream, n_upstream * 4, 4, false}};
-  st = zero::check_arrays(fn, arr, 5, a.ldg == a.in.ld_logits ? 1 : -1, 0);
+  const zero::Arr arr[] = {zero::logits_of(a), zero::dlogits_of(a), zero::label_of(a),
+                           zero::floats("stats", stats, R * ZERO_TOKEN_STATS, false),
+                           zero::floats("upstream", upstream, n_upstream, false)};
+  st = zero::check_arrays(fn, arr, 5, 1, 0);
   if (st != ZERO_OK) return st;
   a.stats_in = stats;
   a.upstream = upstream;
