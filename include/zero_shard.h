@@ -333,6 +333,13 @@ zero_status zero_adam_shard_step_dev_t(const zero_grad_src* src, uint64_t n,
  * that is, the value nearest in square root, halves down; a w above 0 is at least q = 1. The step is
  * 1.6% of the largest for m and 0.8% for w there, and the smallest value 6e-5 and 1.5e-5 of it. A block whose
  * largest is below 2^-126 keeps s = 0 (all zeros), one with a non-finite value s = NaN (all NaN).
+ * What nearest rounding keeps: a moment without a gradient shrinks by a factor f a step (m by beta1, w by sqrt(beta2)), and
+ * index q falls to q - 1 only if 1 - f > 1/q - 1/(4q^2). Indices up to about 1/(1 - f) (9 of m at beta1 0.9; of w 39 at
+ * beta2 0.95, 199 at 0.99, all of them at 0.999) thus keep their share of the block's largest for as long as other elements keep
+ * that up. Where gradients fall unevenly within a block, w stays too large and the steps of those elements too small (beta2
+ * 0.999, half of a block's gradients a tenth: their w is 4.6 times that of 32 bits 3000 steps later; at 0.95 it follows); where
+ * some stop while others go on, a rest of m remains and moves their parameters on by a fraction of lr each step. Gradients
+ * that stay of one size, or change for a whole block, are followed. Tensors of the other kind take state_bits 32.
  * Zeroed bytes and scales are the state of a new parameter. Every operation is fp32, rounded to nearest
  * even on its own, so equal inputs give equal bytes. */
 #define ZERO_STATE8_BLOCK 256

@@ -851,7 +851,8 @@ def adam_tensor(param, grad, m, v, out=None, m_scale=None, v_scale=None, group: 
 
 
 def adam_state(param, bits: int = 32) -> dict:
-    """The state of a new parameter, as keyword arguments of adam_tensor."""
+    """The state of a new parameter, as keyword arguments of adam_tensor. 8 bits suit tensors whose gradients stay of one
+    size or change for 256 elements at once: nearest rounding keeps small shares of a block's largest moment (zero_shard.h)."""
     if bits == 32:
         return {"m": torch.zeros_like(param, dtype=torch.float32), "v": torch.zeros_like(param, dtype=torch.float32)}
     if bits != 8:
