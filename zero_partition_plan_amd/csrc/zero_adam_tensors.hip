@@ -19,6 +19,7 @@
 #include "zero_adam.h"
 #include "zero_device.h"
 #include "zero_internal.h"
+#include "zero_rows.h"
 
 namespace zero {
 namespace {
@@ -69,22 +70,10 @@ __device__ __forceinline__ uint16_t narrow(float x, int32_t dtype) {
   return dtype == ZERO_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x) : __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-// The largest of a wave's magnitudes as bit patterns, in every lane. For patterns without a sign the order
-// of unsigned numbers is that of the values, with a NaN above all.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t larger_moved(uint32_t v) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
-  return o > v ? o : v;
-}
-
-__device__ __forceinline__ float wave_largest(uint32_t v) {
-  v = larger_moved<0x111, 0xf>(v);  // lanes 1, 2, 4, 8 before, in rows of 16
-  v = larger_moved<0x112, 0xf>(v);
-  v = larger_moved<0x114, 0xf>(v);
-  v = larger_moved<0x118, 0xf>(v);
-  v = larger_moved<0x142, 0xa>(v);  // a row's last lane to the next row
-  v = larger_moved<0x143, 0xc>(v);  // lane 31 to the upper rows
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)v, 63));
+// The largest of a wave's magnitudes, in every lane, by their bit patterns: for patterns without a sign the order of
+// unsigned numbers is that of the values, with a NaN above all.
+__device__ __forceinline__ float wave_largest(float v) {
+  return wave_reduce(v, 0.0f, [](float x, float y) { return __float_as_uint(y) > __float_as_uint(x) ? y : x; });
 }
 
 // What of 4 elements' codes and their block's scale is stored.
@@ -105,7 +94,7 @@ __device__ __forceinline__ Coded encode(const float (&x)[4]) {
     const uint32_t mag = __float_as_uint(x[j]) & 0x7fffffffu;
     top = mag > top ? mag : top;
   }
-  const float s = wave_largest(top);
+  const float s = wave_largest(__uint_as_float(top));
   Coded r{0, s};
   if (!(s >= 0x1p-126f && s < INFINITY)) {  // the same in all lanes
     r.scale = s < 0x1p-126f ? 0.0f : NAN;
