@@ -565,7 +565,7 @@ zero_status zero_linear_backward(const zero_linear_shape* s, const void* dy, uin
  *   y = round(residual_scale*x + branch_scale*gate*norm_post(branch))      the stream's type
  *   h = round16(norm_pre(y))                                                of y as it is stored
  * Sums are fp32 in a fixed order; nothing between is rounded to 16 bits. A row whose squares leave fp32 has
- * rstd 0, one of zeros with eps 0 is NaN. */
+ * rstd 0, with eps 0 one whose squares are too small for it has rstd inf, and one of zeros is NaN. */
 
 typedef enum { ZERO_NORM_NONE = 0, ZERO_NORM_RMS = 1, ZERO_NORM_LAYER = 2 } zero_norm;
 

@@ -905,7 +905,9 @@ def zero_adam_tensors_step_dev_t(tensors, grad_scale, table, step, status, wd_mo
 
 class AdamTensorsStep:
     """zero_adam_tensors_step with its tensors marshalled once; a call passes the hyper-parameters of each
-    group and the grad scale. The tensors stay in place while it is used."""
+    group and the grad scale. Marshalling costs the host about 2.5 us a tensor for adam_tensor and 0.25 for the list; a call takes
+    8 us for 48 tensors and 20 for 148 (with a list 20 and 59). It holds its tensors, gradients too, and steps on the memory that
+    it was made with: a program whose gradients are allocated anew each step makes it anew as well, or copies them into place."""
 
     def __init__(self, tensors, skip=None):
         self._tensors, self._skip = _Tensors(tensors), skip

@@ -7,8 +7,8 @@
 // the device and a captured launch holds its own table; a block finds its tensor by halving over the tensors'
 // first blocks. Elementwise streaming, bound by memory. The arithmetic is k_adam_step's, every operation
 // rounded on its own. Measured: the 148 tensors of GPT-2 small (124M elements, 28 bytes each) 563 us, 6.2 TB/s; the 9 of
-// a Llama-7B block (202M, 16 bytes with 8-bit moments) 540, 6.0, where a 2:1 stream reaches 6.0; 48 tensors of 7007
-// elements 6.5, a launch and its chain of loads.
+// a Llama-7B block (202M, 16 bytes with 8-bit moments) 581, 556 at best, 5.6 to 5.8, where a 2:1 stream reaches 6.0; 48 tensors of
+// 7007 elements 6.5, a launch and its chain of loads. That block's codes as numbers 160 us, 6.3 TB/s; numbers as codes 208, 4.9.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(64) void k_tensors(Launch a) {
 }
 
 // Two blocks' codes a wave, both asked for first: the codes are a fifth of the bytes, and one block's are too few in
-// flight (202M codes 172 us, one block a wave 195, four 180).
+// flight (202M codes 160 us, one block a wave 194, four 172).
 constexpr int kValueTiles = 2;
 
 template <int T>

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
 // A row's waves hold 8 columns a lane, or 16. About one block for each compute unit, each for as many rows at a time
 // as it has waves for. Blocks of 16 waves hide more of the loads' latency, those of 8 leave each lane 256 registers
 // in place of 128, which the variants with more sums over rows need (8192 x 4096 bf16 without biases 92 us, 99 in blocks
-// of 8 waves; with two layer norms, their biases and a gate 113, 147 in blocks of 16). Above 8192 columns the sums are
+// of 8 waves; with two layer norms, their biases and a gate 113, 147 in blocks of 16, when that was chosen; 104 by now). Above 8192 columns the sums are
 // formed apart.
 Plan plan_of(uint64_t rows, uint64_t features, uint64_t segment, bool many) {
   Plan p{};

@@ -446,7 +446,7 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
         }
         __syncthreads();
         // a read for each wave up to 8; moves between lanes are the longer chain there (8192 x 4096 with two layer
-        // norms 113 us and 121, but 4096 x 5120 without 73 and 65)
+        // norms 113 us and 121 when that was chosen, but 4096 x 5120 without 73 and 65)
         if (NT > 512 && W > 8) {
 #pragma unroll
           for (int k = 0; k < kOut; k += 4) {
@@ -589,7 +589,7 @@ __global__ __launch_bounds__(NT) void k_backward(BackwardArgs a) {
 
 // The sums over rows where a row takes so many registers that k_backward cannot hold them beside it: each thread
 // walks its 8 columns down the block's rows, with each row's m1 and c1 from k_backward, and reads the arrays
-// again (4096 x 12288 with an fp32 stream and a layer norm 282 us; held in one kernel, and so partly in
+// again (4096 x 12288 with an fp32 stream and a layer norm 278 us; held in one kernel, and so partly in
 // memory, 735).
 constexpr int kColumnThreads = 256;
 
